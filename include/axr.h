@@ -58,7 +58,8 @@ typedef enum axr_status {
   AXR_EWORKSPACE = 4     /* workspace missing or smaller than the matching *_workspace_bytes() */
 } axr_status;
 
-typedef enum axr_dtype { AXR_F32 = 0, AXR_F16 = 1 } axr_dtype;
+/* AXR_BF16 is taken by the paged append and the 8-bit attention; the other entry points refuse it. */
+typedef enum axr_dtype { AXR_F32 = 0, AXR_F16 = 1, AXR_BF16 = 2 } axr_dtype;
 /* Value storage for axr_attend_decode: fp16 rows, quantized rows (the keys' layout), or quantized and tiled
  * (axr_write_values_tiled's layout, d = 128). */
 typedef enum axr_vkind { AXR_V_F16 = 0, AXR_V_QUANT = 1, AXR_V_QUANT_TILED = 2 } axr_vkind;
@@ -72,16 +73,22 @@ AXR_API const char* axr_last_error(void);
  * GPU.  A block that gave up writes NaN into the outputs it owns and sets AXR_STATUS_WAIT_TIMEOUT in the status word
  * of its device; the call that launched it has already returned AXR_OK.  The word is sticky (calls never clear it).
  *
+ * The entry points on device-side tables that check them (axr_append_paged, axr_q8_append_paged,
+ * axr_q8_attend_paged) set AXR_STATUS_BAD_INDEX when a table entry, position or length that they needed was out of
+ * range; what the kernel did in its place is said there.
+ *
  * axr_device_status -- synchronizes the current device (cudaDeviceSynchronize), then copies its status word to
  * *flags [host].  clear != 0 resets the word to 0 after reading.  Returns AXR_ECUDA with a message when
- * AXR_STATUS_WAIT_TIMEOUT is set, AXR_OK otherwise; AXR_EINVAL for a null flags pointer.  A caller that wants to
- * tell a timed-out call from NaN inputs checks the word after the call.
+ * AXR_STATUS_WAIT_TIMEOUT is set, AXR_EINVAL with a message when only AXR_STATUS_BAD_INDEX is, AXR_OK otherwise;
+ * AXR_EINVAL for a null flags pointer.  A caller that wants to tell a timed-out call from NaN inputs checks the word
+ * after the call.
  *
  * axr_selftest_wait_timeout -- the library's test of that give-up path: one block waits on an mbarrier that nothing
  * arrives on (no copy pending), gives up after `polls` polls (1 .. 2^20), sets AXR_STATUS_WAIT_TIMEOUT and returns.
  * The GPU context stays usable.  Asynchronous on `stream`.  Not part of the method.
  */
 #define AXR_STATUS_WAIT_TIMEOUT 1u
+#define AXR_STATUS_BAD_INDEX 2u
 AXR_API axr_status axr_device_status(unsigned int* flags, int clear);
 AXR_API axr_status axr_selftest_wait_timeout(int polls, void* stream);
 
@@ -360,6 +367,88 @@ AXR_API axr_status axr_pot_attend_decode(const float* q, const uint8_t* codes, c
                                          const uint16_t* v, const int32_t* seq_lens, int B, int Hq, int Hkv, int T,
                                          int Tcap, int d, int E, int M, float scale, float* out, void* workspace,
                                          size_t ws_bytes, void* stream);
+
+/*
+ * New tokens into paged caches, and an 8-bit paged cache.  A server's step has the raw projections q, k, v of a ragged
+ * batch (one token of each decoding sequence, chunks of prompts) and needs them rotated by their positions and in the
+ * cache.  The pages quantize each token once on write (AXELRAM Key Points, 2nd item); the rotation, the ragged batch
+ * and the 8-bit format are not on them.
+ *
+ * Arguments shared by the three entry points:
+ *   q, k, v      [dev] token rows of Hq, Hkv and Hkv heads of d coordinates (x_dtype: AXR_F32, AXR_F16 or AXR_BF16),
+ *                16-byte aligned, token i at element offset i * stride (slices of one fused projection row qualify:
+ *                strides are at least a token's heads and multiples of 16 bytes);
+ *   cu_new/cu_q  [dev] [B + 1] int32, non-decreasing: sequence b's tokens are cu[b] .. cu[b + 1] - 1; NULL: one token
+ *                per sequence (n_tok = B).  Tokens at or past cu[B] belong to no sequence: nothing of theirs is read
+ *                into the cache, and their output rows are left as they are;
+ *   seq_lens     [dev] [B] int32, lengths with the new tokens: token i of sequence b has cache position
+ *                seq_lens[b] - (cu[b + 1] - cu[b]) + (i - cu[b]);
+ *   block_table  [dev] [B, max_blocks] int32, pool block of each logical block; block_tokens a power of two in
+ *                [16, 2^20]; num_blocks the pools' block count;
+ *   cos_sin      [dev] [max_pos, rot] f32: row p holds the rot / 2 cosines, then the rot / 2 sines of position p's
+ *                angles; rot a multiple of 16 up to d.  Pairs are (j, j + rot / 2), or (2 j, 2 j + 1) with interleaved
+ *                != 0: (a, b) -> (a c - b s, b c + a s), each product and sum rounded to fp32 by itself; coordinates
+ *                at or past rot stay.  NULL: no rotation (and no q);
+ *   positions    [dev] [n_tok] int32 rotation positions, or NULL: the cache positions;
+ *   q_out        [dev] out, the rotated queries, contiguous; NULL together with q.
+ * Tokens whose cache position is negative are skipped.  Tokens past the block table's reach, with a table entry outside
+ * [0, num_blocks) or a rotation position outside [0, max_pos) are skipped and set AXR_STATUS_BAD_INDEX.  No two
+ * sequences may have new tokens in one pool block.  Inputs must be finite: in the 8-bit cache NaN is held as 0 and an
+ * infinity as the block's largest code (neither counts towards its scale).
+ *
+ * axr_append_paged -- keys through the write path of axr_write_keys on the rotated key (the same codes and norms, bit
+ *   for bit), values the same way (AXR_V_QUANT) or as fp16 rounded to nearest even (AXR_V_F16), into the pools of
+ *   axr_attend_decode_paged.  q_out is fp32 whatever x_dtype, as the decode entry points take it.
+ *
+ * The 8-bit cache: codes [num_blocks, Hkv, bt, d] (kind AXR_Q8_INT: int8 in [-127, 127]; AXR_Q8_E4M3: e4m3 floats) and
+ * one fp32 scale for each block of 16 tokens and KV head, [num_blocks, Hkv, bt / 16]; a coordinate is code * scale.
+ *
+ * axr_q8_append_paged -- for each 16-token block and head that gets new tokens (keys after rotation):
+ *     need = max |x| / 127 (int8), or the smallest power of two >= max |x| / 448 (e4m3); 0 when max |x| < 2^-100;
+ *     s = max(s_old, need), s_old the block's scale if older tokens live in it, else 0;
+ *     code = rne(x * (1 / s)), clamped to the largest code; when s > s_old, the older tokens' codes become
+ *     rne(code * (s_old * (1 / s))).
+ *   Every step is one fp32 operation.  A growth of an e4m3 block is exact but for subnormal codes; a growth of an int8
+ *   block costs its older tokens up to half a code more.  Rows of a block that no token has reached keep their bytes.
+ *   q_out has x_dtype.
+ *
+ * axr_q8_attend_paged -- causal attention of the query tokens over the 8-bit cache that holds them already: token i of
+ *   sequence b sees the cache positions up to its own.  out [n_tok, Hq, d] of x_dtype.  Sums and softmax statistics
+ *   are fp32; queries and weights enter the tensor cores as hi and lo fp16 planes (about 22 bits).  A token that sees
+ *   nothing (seq_lens[b] smaller than its sequence's token count) gets 0.
+ *   max_q an upper bound of a sequence's query tokens, or 0 if unknown; rows of a longer sequence are not written (and
+ *   AXR_STATUS_BAD_INDEX is set).  T an upper bound of the lengths (longer ones are cut to it); seq_lens NULL: all T.
+ *   A table entry outside [0, num_blocks) reads block 0 and sets AXR_STATUS_BAD_INDEX.  Cache rows at or past a
+ *   sequence's length may hold anything.  G = Hq / Hkv in 1 .. 16.
+ *   workspace [dev] >= axr_q8_attend_workspace_bytes(n_tok, max_q, B, Hq, Hkv, T, d) bytes (max_q = 1 without cu_q),
+ *   16-aligned; may be NULL when that is 0.
+ *
+ * Errors: AXR_EINVAL (pointers, sizes, strides, alignment, dtype, kind), AXR_EUNSUPPORTED (d not in {64, 128}, bits,
+ * rot, G), AXR_EWORKSPACE, AXR_ECUDA.  n_tok == 0 or B == 0 is a no-op.
+ */
+#define AXR_Q8_INT 0
+#define AXR_Q8_E4M3 1
+AXR_API axr_status axr_append_paged(const void* q, const void* k, const void* v, axr_dtype x_dtype, int64_t q_stride,
+                                    int64_t k_stride, int64_t v_stride, const float* cos_sin, int64_t max_pos,
+                                    int rot, int interleaved, const int32_t* positions, const int32_t* cu_new,
+                                    const int32_t* seq_lens, int64_t n_tok, int B, int Hq, int Hkv, int d, int bits,
+                                    const int8_t* signs, uint8_t* kcodes, uint16_t* knorms, axr_vkind vkind,
+                                    void* values, uint16_t* vnorms, const int32_t* block_table, int max_blocks,
+                                    int block_tokens, int num_blocks, float* q_out, void* stream);
+AXR_API axr_status axr_q8_append_paged(const void* q, const void* k, const void* v, axr_dtype x_dtype,
+                                       int64_t q_stride, int64_t k_stride, int64_t v_stride, const float* cos_sin,
+                                       int64_t max_pos, int rot, int interleaved, const int32_t* positions,
+                                       const int32_t* cu_new, const int32_t* seq_lens, int64_t n_tok, int B, int Hq,
+                                       int Hkv, int d, int kind, uint8_t* kcodes, float* kscales, uint8_t* vcodes,
+                                       float* vscales, const int32_t* block_table, int max_blocks, int block_tokens,
+                                       int num_blocks, void* q_out, void* stream);
+AXR_API size_t axr_q8_attend_workspace_bytes(int64_t n_tok, int max_q, int B, int Hq, int Hkv, int T, int d);
+AXR_API axr_status axr_q8_attend_paged(const void* q, axr_dtype x_dtype, int64_t q_stride, const uint8_t* kcodes,
+                                       const float* kscales, const uint8_t* vcodes, const float* vscales, int kind,
+                                       const int32_t* block_table, int max_blocks, int block_tokens, int num_blocks,
+                                       const int32_t* cu_q, const int32_t* seq_lens, int64_t n_tok, int max_q, int B,
+                                       int Hq, int Hkv, int T, int d, float scale, void* out, void* workspace,
+                                       size_t ws_bytes, void* stream);
 
 /* Bytes of workspace for axr_select_signs with these sizes. */
 AXR_API size_t axr_select_workspace_bytes(int n_layers, int n_seq, int n_tok, int Hq, int Hkv, int d, int n_cand);

@@ -13,10 +13,12 @@ _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libaxr.so")
 
 STATUS = {0: "AXR_OK", 1: "AXR_EINVAL", 2: "AXR_EUNSUPPORTED", 3: "AXR_ECUDA", 4: "AXR_EWORKSPACE"}
-F32, F16 = 0, 1
+F32, F16, BF16 = 0, 1, 2
 V_F16, V_QUANT, V_QUANT_TILED = 0, 1, 2
 GATHER_FACTORED, GATHER_TABLE, GATHER_TENSOR, GATHER_MMA, GATHER_DIRECT = 0, 1, 2, 3, 4
 STATUS_WAIT_TIMEOUT = 1
+STATUS_BAD_INDEX = 2
+Q8_INT, Q8_E4M3 = 0, 1
 
 _p = ctypes.c_void_p
 _i = ctypes.c_int
@@ -53,6 +55,13 @@ SIGNATURES = {
     "axr_pot_write": (_i, [_p, _i64, _i, _i, _i, _p, _p, _p, _p]),
     "axr_pot_score": (_i, [_p, _p, _p, _p, _i, _i, _i, _i, _i, _i, _i, _i, _f, _p, _p, _p]),
     "axr_pot_attend_decode": (_i, [_p, _p, _p, _p, _p, _i, _i, _i, _i, _i, _i, _i, _i, _f, _p, _p, _sz, _p]),
+    "axr_append_paged": (_i, [_p, _p, _p, _i, _i64, _i64, _i64, _p, _i64, _i, _i, _p, _p, _p, _i64, _i, _i, _i, _i, _i,
+                              _p, _p, _p, _i, _p, _p, _p, _i, _i, _i, _p, _p]),
+    "axr_q8_append_paged": (_i, [_p, _p, _p, _i, _i64, _i64, _i64, _p, _i64, _i, _i, _p, _p, _p, _i64, _i, _i, _i, _i,
+                                 _i, _p, _p, _p, _p, _p, _i, _i, _i, _p, _p]),
+    "axr_q8_attend_workspace_bytes": (_sz, [_i64, _i, _i, _i, _i, _i, _i]),
+    "axr_q8_attend_paged": (_i, [_p, _i, _i64, _p, _p, _p, _p, _i, _p, _i, _i, _i, _p, _p, _i64, _i, _i, _i, _i, _i, _i,
+                                 _f, _p, _p, _sz, _p]),
     "axr_set_gather": (_i, [_i]),
     "axr_device_status": (_i, [_p, _i]),
     "axr_selftest_wait_timeout": (_i, [_i, _p]),

@@ -1,0 +1,141 @@
+// axr_q8_attend_paged: argument checks, the choice of kernels and the split of the token axis.
+#include <cmath>
+
+#include "axr_host.h"
+#include "paged_host.h"
+#include "q8_decode.cuh"
+
+namespace axr {
+namespace {
+
+constexpr int kDecodeThreads = 128;
+constexpr int kDecodeWorkers = kSmCount * 8;
+
+// Row groups of 8 and tiles of a call.
+struct Q8Plan {
+  Q8Tiles tl;
+  int nrg;
+  SplitPlan sp;
+};
+
+Q8Plan plan_decode(int64_t n_tok, int B, int G, int Hkv, int T, bool one, int max_q) {
+  Q8Plan pl;
+  pl.nrg = (one ? static_cast<int64_t>(max_q) * G <= 8 : G <= 8 && n_tok <= B) ? 1 : 2;
+  pl.tl.tpt = 8 * pl.nrg / G;
+  pl.tl.one = one;
+  pl.tl.skip_long = false;
+  pl.tl.skip_short = 0;
+  pl.tl.tiles = one ? B : n_tok / pl.tl.tpt + B;
+  const int64_t units = pl.tl.tiles < 65536 ? pl.tl.tiles : 65536;
+  pl.sp = plan_splits(static_cast<int>(units), Hkv, T, kDecodeWorkers, 32, 2, 2.0);
+  return pl;
+}
+
+size_t partial_bytes(const Q8Plan& pl, int Hkv, int d) {
+  if (pl.sp.splits == 1) return 0;
+  const size_t parts = static_cast<size_t>(pl.tl.tiles) * Hkv * 8 * pl.nrg * pl.sp.splits;
+  return (parts * (static_cast<size_t>(d) + 2) * sizeof(float) + 255) / 256 * 256;
+}
+
+template <typename T, int D, bool I8, int NRG>
+axr_status launch(const Q8Attend& a, const Q8Plan& pl, cudaStream_t st, const char* w) {
+  const int64_t items = pl.tl.tiles * a.Hkv * a.splits;
+  const int per = kDecodeThreads / 32;
+  int64_t grid = (items + per - 1) / per;
+  if (grid > kSmCount * 4) grid = kSmCount * 4;
+  q8_decode_kernel<T, D, I8, NRG><<<static_cast<unsigned>(grid), kDecodeThreads, 0, st>>>(a, pl.tl);
+  if (a.splits > 1)
+    q8_merge_kernel<T, D><<<static_cast<unsigned>(pl.tl.tiles * a.Hkv * 8 * NRG), D, 0, st>>>(a, pl.tl, 8 * NRG);
+  return check_launch(w);
+}
+
+template <typename T, int D, bool I8>
+axr_status by_rows(const Q8Attend& a, const Q8Plan& pl, cudaStream_t st, const char* w) {
+  return pl.nrg == 1 ? launch<T, D, I8, 1>(a, pl, st, w) : launch<T, D, I8, 2>(a, pl, st, w);
+}
+
+template <typename T>
+axr_status by_kind(int d, int kind, const Q8Attend& a, const Q8Plan& pl, cudaStream_t st, const char* w) {
+  const bool i8 = kind == AXR_Q8_INT;
+  if (d == 64) return i8 ? by_rows<T, 64, true>(a, pl, st, w) : by_rows<T, 64, false>(a, pl, st, w);
+  return i8 ? by_rows<T, 128, true>(a, pl, st, w) : by_rows<T, 128, false>(a, pl, st, w);
+}
+
+bool one_tile(bool ragged, int max_q, int G) { return !ragged || (max_q > 0 && static_cast<int64_t>(max_q) * G <= 16); }
+
+}  // namespace
+}  // namespace axr
+
+extern "C" size_t axr_q8_attend_workspace_bytes(int64_t n_tok, int max_q, int B, int Hq, int Hkv, int T, int d) {
+  using namespace axr;
+  if (n_tok <= 0 || n_tok > 0x7fffffff || B <= 0 || Hkv <= 0 || Hq <= 0 || Hq % Hkv || Hq / Hkv > 16 || T <= 0 ||
+      d <= 0 || max_q < 0)
+    return 0;
+  const int G = Hq / Hkv;
+  const bool one = one_tile(true, max_q, G);
+  return partial_bytes(plan_decode(n_tok, B, G, Hkv, T, one, max_q), Hkv, d);
+}
+
+extern "C" axr_status axr_q8_attend_paged(const void* q, axr_dtype x_dtype, int64_t q_stride, const uint8_t* kcodes,
+                                          const float* kscales, const uint8_t* vcodes, const float* vscales,
+                                          int kind, const int32_t* block_table, int max_blocks, int block_tokens,
+                                          int num_blocks, const int32_t* cu_q, const int32_t* seq_lens,
+                                          int64_t n_tok, int max_q, int B, int Hq, int Hkv, int T, int d, float scale,
+                                          void* out, void* workspace, size_t ws_bytes, void* stream) {
+  using namespace axr;
+  const char* w = "axr_q8_attend_paged";
+  if (x_dtype != AXR_F32 && x_dtype != AXR_F16 && x_dtype != AXR_BF16)
+    return set_error(AXR_EINVAL, "%s: bad dtype", w);
+  if (kind != AXR_Q8_INT && kind != AXR_Q8_E4M3) return set_error(AXR_EINVAL, "%s: bad kind %d", w, kind);
+  if (n_tok < 0 || n_tok > 0x7fffffff || B < 0 || B > (1 << 24) || Hq <= 0 || Hkv <= 0 || Hkv > 65535 || T < 0 ||
+      max_q < 0)
+    return set_error(AXR_EINVAL, "%s: bad sizes n_tok=%lld max_q=%d B=%d Hq=%d Hkv=%d T=%d", w,
+                     static_cast<long long>(n_tok), max_q, B, Hq, Hkv, T);
+  if (Hq % Hkv) return set_error(AXR_EINVAL, "%s: Hq=%d is not a multiple of Hkv=%d", w, Hq, Hkv);
+  if (d != 64 && d != 128) return set_error(AXR_EUNSUPPORTED, "%s: d=%d not in {64,128}", w, d);
+  const int G = Hq / Hkv;
+  if (G > 16) return set_error(AXR_EUNSUPPORTED, "%s: G=%d above 16", w, G);
+  if (!cu_q && n_tok != B)
+    return set_error(AXR_EINVAL, "%s: without cu_q there is one token per sequence (n_tok=%lld, B=%d)", w,
+                     static_cast<long long>(n_tok), B);
+  int shift = 0;
+  axr_status st = check_table(w, block_table, max_blocks, block_tokens, num_blocks, &shift);
+  if (st != AXR_OK) return st;
+  if (static_cast<int64_t>(T) > static_cast<int64_t>(max_blocks) * block_tokens)
+    return set_error(AXR_EINVAL, "%s: T=%d exceeds max_blocks=%d x block_tokens=%d", w, T, max_blocks, block_tokens);
+  if (!std::isfinite(scale)) return set_error(AXR_EINVAL, "%s: scale is not finite", w);
+  if (n_tok == 0 || B == 0) return set_error(AXR_OK, "");
+  if (!q || !kcodes || !kscales || !vcodes || !vscales || !out) return set_error(AXR_EINVAL, "%s: null pointer", w);
+  if (!aligned(q, 16) || !aligned(kcodes, 16) || !aligned(vcodes, 16) || !aligned(kscales, 4) ||
+      !aligned(vscales, 4) || !aligned(out, 16) || (cu_q && !aligned(cu_q, 4)) || (seq_lens && !aligned(seq_lens, 4)))
+    return set_error(AXR_EINVAL, "%s: misaligned pointer", w);
+  if (q_stride < static_cast<int64_t>(Hq) * d || q_stride % (16 / static_cast<int64_t>(dtype_bytes(x_dtype))))
+    return set_error(AXR_EINVAL, "%s: the token stride is below a token's heads or not a multiple of 16 bytes", w);
+  if (!cu_q) max_q = 1;
+  Q8Attend a;
+  memset(&a, 0, sizeof(a));
+  a.q = q; a.q_stride = q_stride; a.kcodes = kcodes; a.vcodes = vcodes; a.kscales = kscales; a.vscales = vscales;
+  a.table = block_table; a.cu = cu_q; a.seq_lens = seq_lens; a.out = out; a.n_tok = n_tok;
+  a.B = B; a.Hq = Hq; a.Hkv = Hkv; a.G = G; a.T = T; a.max_blocks = max_blocks; a.shift = shift;
+  a.num_blocks = num_blocks; a.mult = scale * kQ8Log2e;
+  const Q8Plan pl = plan_decode(n_tok, B, G, Hkv, T > 0 ? T : 1, one_tile(cu_q != nullptr, max_q, G), max_q);
+  if (pl.tl.tiles * Hkv * 8 * pl.nrg > 0x7fffffff) return set_error(AXR_EUNSUPPORTED, "%s: too many rows", w);
+  a.splits = pl.sp.splits;
+  a.chunk = pl.sp.chunk;
+  const size_t need = partial_bytes(pl, Hkv, d);
+  if (need) {
+    if (!workspace || ws_bytes < need)
+      return set_error(AXR_EWORKSPACE, "%s: workspace of %zu bytes, need %zu", w, workspace ? ws_bytes : 0, need);
+    if (!aligned(workspace, 16)) return set_error(AXR_EINVAL, "%s: workspace not 16-byte aligned", w);
+    const size_t parts = static_cast<size_t>(pl.tl.tiles) * Hkv * 8 * pl.nrg * a.splits;
+    a.ws_o = static_cast<float*>(workspace);
+    a.ws_m = a.ws_o + parts * d;
+    a.ws_l = a.ws_m + parts;
+  }
+  a.status = status_word();
+  if (!a.status) return set_error(AXR_ECUDA, "%s: the status word has no device address", w);
+  cudaStream_t s = as_stream(stream);
+  if (x_dtype == AXR_F16) return by_kind<__half>(d, kind, a, pl, s, w);
+  if (x_dtype == AXR_BF16) return by_kind<__nv_bfloat16>(d, kind, a, pl, s, w);
+  return by_kind<float>(d, kind, a, pl, s, w);
+}

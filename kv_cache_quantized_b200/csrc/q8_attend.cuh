@@ -1,0 +1,115 @@
+// Attention over the paged 8-bit cache (q8.cuh): arguments and helpers shared by its kernels.
+//
+// Query row r = (token i, head g) of a sequence and KV head sees keys 0 .. pos0 + i, pos0 = len - count:
+//   s_t = scale * ks_t (q . code^K_t),   o = sum_t 2^(s_t log2 e - m) vs_t code^V_t / sum_t 2^(s_t log2 e - m)
+// with ks_t, vs_t the scales of token t's 16-token block.
+#pragma once
+
+#include "paged_new.cuh"
+#include "q8.cuh"
+
+namespace axr {
+
+constexpr float kQ8Log2e = 1.4426950408889634f;
+
+struct Q8Attend {
+  const void* q;            // token rows of q_stride elements, [Hq, D] each
+  int64_t q_stride;
+  const uint8_t *kcodes, *vcodes;
+  const float *kscales, *vscales;
+  const int32_t* table;     // [B, max_blocks]
+  const int32_t* cu;        // [B + 1] or null: one query token per sequence
+  const int32_t* seq_lens;  // [B] or null: T
+  void* out;                // [n_tok, Hq, D]
+  float *ws_o, *ws_m, *ws_l;  // [tiles, Hkv, rows, splits, D], [tiles, Hkv, rows, splits] x 2
+  int64_t n_tok;
+  int B, Hq, Hkv, G, T, max_blocks, shift, num_blocks;
+  int splits, chunk;        // the token axis: splits chunks of `chunk` tokens
+  float mult;               // scale * log2 e
+  unsigned int* status;
+};
+
+// One sequence's query tokens and length.
+struct Q8Span {
+  int64_t first;  // first flat token
+  int count, pos0, len;
+};
+
+__device__ __forceinline__ Q8Span q8_span(const Q8Attend& a, int b) {
+  Q8Span s;
+  const int len = a.seq_lens ? a.seq_lens[b] : a.T;
+  int64_t lo = b, hi = static_cast<int64_t>(b) + 1;
+  if (a.cu) {
+    lo = a.cu[b];
+    hi = a.cu[b + 1];
+    if (lo < 0 || hi > a.n_tok || hi < lo) lo = hi = 0;
+  }
+  s.first = lo;
+  s.count = static_cast<int>(hi - lo);
+  s.len = max(0, min(len, a.T));
+  s.pos0 = s.len - s.count;
+  return s;
+}
+
+// How a kernel cuts the query tokens into row tiles of up to tpt tokens (times the heads of a group).
+//  one  = true:  tile b is sequence b, which has at most tpt tokens; longer sequences are another kernel's (skip_long)
+//                or break the caller's bound (flagged in the status word);
+//  one  = false: sequence b owns the tiles from cu[b] / tpt + b on: at most n_tok / tpt + B tiles in all, found
+//                without knowing the lengths on the host.  Sequences of at most skip_short tokens are skipped.
+struct Q8Tiles {
+  int64_t tiles;
+  int tpt;
+  bool one, skip_long;
+  int skip_short;
+};
+
+// Sequence and first token of a tile.  One warp.
+__device__ __forceinline__ void q8_tile(const Q8Attend& a, const Q8Tiles& tl, int64_t tile, int lane, int& b,
+                                        int64_t& i0) {
+  b = static_cast<int>(tile);
+  i0 = 0;
+  if (!tl.one) {
+    auto start = [&](int s) { return static_cast<int64_t>(a.cu[s]) / tl.tpt + s; };
+    b = last_at_most(a.B, tile, lane, start);
+    i0 = (tile - start(b)) * tl.tpt;
+  }
+}
+
+__device__ __forceinline__ bool q8_tile_live(const Q8Attend& a, const Q8Tiles& tl, const Q8Span& sp, int64_t i0,
+                                             int lane) {
+  if (tl.one && sp.count > tl.tpt) {
+    if (!tl.skip_long && lane == 0) atomicOr(a.status, kStatusBadIndex);
+    return false;
+  }
+  return i0 >= 0 && i0 < sp.count && sp.count > tl.skip_short;
+}
+
+// Pool row (in tokens, KV head hk) of cache position t of sequence b; an entry outside the pools reads block 0 and
+// sets the status word.
+__device__ __forceinline__ int64_t q8_row(const Q8Attend& a, int b, int hk, int t) {
+  int page = __ldg(a.table + static_cast<size_t>(b) * a.max_blocks + (t >> a.shift));
+  if (page < 0 || page >= a.num_blocks) {
+    atomicOr(a.status, kStatusBadIndex);
+    page = 0;
+  }
+  return ((static_cast<int64_t>(page) * a.Hkv + hk) << a.shift) + (t & ((1 << a.shift) - 1));
+}
+
+template <typename T>
+__device__ __forceinline__ float to_float(T x);
+template <>
+__device__ __forceinline__ float to_float<float>(float x) { return x; }
+template <>
+__device__ __forceinline__ float to_float<__half>(__half x) { return __half2float(x); }
+template <>
+__device__ __forceinline__ float to_float<__nv_bfloat16>(__nv_bfloat16 x) { return __bfloat162float(x); }
+template <typename T>
+__device__ __forceinline__ T from_float(float x);
+template <>
+__device__ __forceinline__ float from_float<float>(float x) { return x; }
+template <>
+__device__ __forceinline__ __half from_float<__half>(float x) { return __float2half_rn(x); }
+template <>
+__device__ __forceinline__ __nv_bfloat16 from_float<__nv_bfloat16>(float x) { return __float2bfloat16_rn(x); }
+
+}  // namespace axr

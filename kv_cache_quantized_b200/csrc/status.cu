@@ -61,6 +61,10 @@ extern "C" axr_status axr_device_status(unsigned int* flags, int clear) {
     return set_error(AXR_ECUDA,
                      "axr_device_status: a bounded wait in a kernel gave up (a copy or a stage did not arrive in "
                      "about a second); the outputs of the affected calls hold NaN");
+  if (*flags & AXR_STATUS_BAD_INDEX)
+    return set_error(AXR_EINVAL,
+                     "axr_device_status: a block table entry, a position or a length that a call needed was out of "
+                     "range");
   return set_error(AXR_OK, "");
 }
 

@@ -7,6 +7,8 @@
 // codes packed as an LSB-first bitstream (coordinate j at bits [j b, j b + b)).
 #pragma once
 
+#include <cuda_bf16.h>
+
 #include "axr_common.cuh"
 
 namespace axr {
@@ -45,21 +47,26 @@ __device__ __forceinline__ void load_lane<__half, 1>(const __half* row, int lane
   v[0] = __half2float(row[lane]);
 }
 
-// Codes of one vector into idx (shared memory, one byte per coordinate); returns ||x||.  Whole warp.
-template <int D, int BITS, typename TIn>
-__device__ __forceinline__ float quantize_vector(const TIn* __restrict__ xrow, const float (&sg)[WarpVec<D>::VPL],
-                                                 const float (&tau)[(1 << BITS) - 1], int lane, uint8_t* idx) {
+template <>
+__device__ __forceinline__ void load_lane<__nv_bfloat16, 4>(const __nv_bfloat16* row, int lane, float (&v)[4]) {
+  uint2 a = reinterpret_cast<const uint2*>(row)[lane];
+  float2 lo = __bfloat1622float2(*reinterpret_cast<__nv_bfloat162*>(&a.x));
+  float2 hi = __bfloat1622float2(*reinterpret_cast<__nv_bfloat162*>(&a.y));
+  v[0] = lo.x; v[1] = lo.y; v[2] = hi.x; v[3] = hi.y;
+}
+template <>
+__device__ __forceinline__ void load_lane<__nv_bfloat16, 2>(const __nv_bfloat16* row, int lane, float (&v)[2]) {
+  float2 a = __bfloat1622float2(reinterpret_cast<const __nv_bfloat162*>(row)[lane]);
+  v[0] = a.x; v[1] = a.y;
+}
+
+// The lane's coordinates v (lanes below LANES; zeros elsewhere) to its codes q; returns ||x||.  Whole warp.
+template <int D, int BITS>
+__device__ __forceinline__ float quantize_lane(float (&v)[WarpVec<D>::VPL], const float (&sg)[WarpVec<D>::VPL],
+                                               const float (&tau)[(1 << BITS) - 1], int lane,
+                                               int (&code)[WarpVec<D>::VPL]) {
   constexpr int VPL = WarpVec<D>::VPL;
-  constexpr int LANES = WarpVec<D>::LANES;
   constexpr int L = 1 << BITS;
-  const bool active = lane < LANES;
-  float v[VPL];
-  if (active) {
-    load_lane<TIn, VPL>(xrow, lane, v);
-  } else {
-#pragma unroll
-    for (int i = 0; i < VPL; ++i) v[i] = 0.0f;
-  }
   float ss = 0.0f;
 #pragma unroll
   for (int i = 0; i < VPL; ++i) {
@@ -69,15 +76,35 @@ __device__ __forceinline__ float quantize_vector(const TIn* __restrict__ xrow, c
   ss = warp_sum(ss);
   const float n = sqrtf(ss);
   fwht_warp<D>(v, lane);  // v = FWHT(s .* x) = sqrt(D) * H (s .* x)
+#pragma unroll
+  for (int i = 0; i < VPL; ++i) {
+    const float w = n > 0.0f ? v[i] / n : 0.0f;  // = sqrt(D) * u
+    int q = 0;
+#pragma unroll
+    for (int k = 0; k < L - 1; ++k) q += (w >= tau[k]) ? 1 : 0;
+    code[i] = q;
+  }
+  return n;
+}
+
+// Codes of one vector into idx (shared memory, one byte per coordinate); returns ||x||.  Whole warp.
+template <int D, int BITS, typename TIn>
+__device__ __forceinline__ float quantize_vector(const TIn* __restrict__ xrow, const float (&sg)[WarpVec<D>::VPL],
+                                                 const float (&tau)[(1 << BITS) - 1], int lane, uint8_t* idx) {
+  constexpr int VPL = WarpVec<D>::VPL;
+  const bool active = lane < WarpVec<D>::LANES;
+  float v[VPL];
+  if (active) {
+    load_lane<TIn, VPL>(xrow, lane, v);
+  } else {
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) v[i] = 0.0f;
+  }
+  int code[VPL];
+  const float n = quantize_lane<D, BITS>(v, sg, tau, lane, code);
   if (active) {
 #pragma unroll
-    for (int i = 0; i < VPL; ++i) {
-      const float w = n > 0.0f ? v[i] / n : 0.0f;  // = sqrt(D) * u
-      int q = 0;
-#pragma unroll
-      for (int k = 0; k < L - 1; ++k) q += (w >= tau[k]) ? 1 : 0;
-      idx[lane * VPL + i] = static_cast<uint8_t>(q);
-    }
+    for (int i = 0; i < VPL; ++i) idx[lane * VPL + i] = static_cast<uint8_t>(code[i]);
   }
   return n;
 }
