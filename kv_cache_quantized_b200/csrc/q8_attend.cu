@@ -31,6 +31,21 @@ Q8Plan plan_decode(int64_t n_tok, int B, int G, int Hkv, int T, bool one, int ma
   return pl;
 }
 
+// The tcgen05 kernel: tiles of 128 rows, two thread blocks per SM, splits of at least two key tiles; a block's set-up
+// (query operand, first code tiles) costs about two key tiles.
+Q8Plan plan_prefill(int64_t n_tok, int B, int G, int Hkv, int T) {
+  Q8Plan pl;
+  pl.nrg = kQ8PrefillRows / 8;
+  pl.tl.tpt = kQ8PrefillRows / G;
+  pl.tl.one = false;
+  pl.tl.skip_long = false;
+  pl.tl.skip_short = 0;
+  pl.tl.tiles = n_tok / pl.tl.tpt + B;
+  const int64_t units = pl.tl.tiles < 65536 ? pl.tl.tiles : 65536;
+  pl.sp = plan_splits(static_cast<int>(units), Hkv, T, 2 * kSmCount, 128, 2, 2.0);
+  return pl;
+}
+
 size_t partial_bytes(const Q8Plan& pl, int Hkv, int d) {
   if (pl.sp.splits == 1) return 0;
   const size_t parts = static_cast<size_t>(pl.tl.tiles) * Hkv * 8 * pl.nrg * pl.sp.splits;
@@ -72,8 +87,11 @@ extern "C" size_t axr_q8_attend_workspace_bytes(int64_t n_tok, int max_q, int B,
       d <= 0 || max_q < 0)
     return 0;
   const int G = Hq / Hkv;
+  if (max_q == 0 || max_q > n_tok) max_q = static_cast<int>(n_tok);
   const bool one = one_tile(true, max_q, G);
-  return partial_bytes(plan_decode(n_tok, B, G, Hkv, T, one, max_q), Hkv, d);
+  const size_t x = partial_bytes(plan_decode(n_tok, B, G, Hkv, T, one, max_q), Hkv, d);
+  const size_t y = one ? 0 : partial_bytes(plan_prefill(n_tok, B, G, Hkv, T), Hkv, d);
+  return x > y ? x : y;
 }
 
 extern "C" axr_status axr_q8_attend_paged(const void* q, axr_dtype x_dtype, int64_t q_stride, const uint8_t* kcodes,
@@ -112,14 +130,19 @@ extern "C" axr_status axr_q8_attend_paged(const void* q, axr_dtype x_dtype, int6
   if (q_stride < static_cast<int64_t>(Hq) * d || q_stride % (16 / static_cast<int64_t>(dtype_bytes(x_dtype))))
     return set_error(AXR_EINVAL, "%s: the token stride is below a token's heads or not a multiple of 16 bytes", w);
   if (!cu_q) max_q = 1;
+  if (max_q == 0 || max_q > n_tok) max_q = static_cast<int>(n_tok);
   Q8Attend a;
   memset(&a, 0, sizeof(a));
   a.q = q; a.q_stride = q_stride; a.kcodes = kcodes; a.vcodes = vcodes; a.kscales = kscales; a.vscales = vscales;
   a.table = block_table; a.cu = cu_q; a.seq_lens = seq_lens; a.out = out; a.n_tok = n_tok;
   a.B = B; a.Hq = Hq; a.Hkv = Hkv; a.G = G; a.T = T; a.max_blocks = max_blocks; a.shift = shift;
   a.num_blocks = num_blocks; a.mult = scale * kQ8Log2e;
-  const Q8Plan pl = plan_decode(n_tok, B, G, Hkv, T > 0 ? T : 1, one_tile(cu_q != nullptr, max_q, G), max_q);
-  if (pl.tl.tiles * Hkv * 8 * pl.nrg > 0x7fffffff) return set_error(AXR_EUNSUPPORTED, "%s: too many rows", w);
+  // up to 16 query rows per sequence and KV head: the warp-MMA kernel, one tile a sequence; more: the tcgen05 kernel,
+  // or, for fp32 queries and outputs (which its fp16 weights could not serve), the warp-MMA kernel over flat tiles
+  const bool one = one_tile(cu_q != nullptr, max_q, G), prefill = !one && x_dtype != AXR_F32;
+  const Q8Plan pl = prefill ? plan_prefill(n_tok, B, G, Hkv, T > 0 ? T : 1)
+                            : plan_decode(n_tok, B, G, Hkv, T > 0 ? T : 1, one, max_q);
+  if (pl.tl.tiles * Hkv * 8 * pl.nrg > 0x7fffffff || pl.tl.tiles * Hkv * pl.sp.splits > 0x7fffffff) return set_error(AXR_EUNSUPPORTED, "%s: too many rows", w);
   a.splits = pl.sp.splits;
   a.chunk = pl.sp.chunk;
   const size_t need = partial_bytes(pl, Hkv, d);
@@ -135,6 +158,7 @@ extern "C" axr_status axr_q8_attend_paged(const void* q, axr_dtype x_dtype, int6
   a.status = status_word();
   if (!a.status) return set_error(AXR_ECUDA, "%s: the status word has no device address", w);
   cudaStream_t s = as_stream(stream);
+  if (prefill) return q8_prefill_launch(x_dtype == AXR_F16, d, kind == AXR_Q8_INT, a, pl.tl, s, w);
   if (x_dtype == AXR_F16) return by_kind<__half>(d, kind, a, pl, s, w);
   if (x_dtype == AXR_BF16) return by_kind<__nv_bfloat16>(d, kind, a, pl, s, w);
   return by_kind<float>(d, kind, a, pl, s, w);

@@ -1,0 +1,34 @@
+// Launcher of the tcgen05 attention over the 8-bit cache (q8_prefill.cuh).
+#include "launch.h"
+#include "q8_merge.cuh"
+#include "q8_prefill.cuh"
+
+namespace axr {
+namespace {
+
+template <typename T, int D, bool I8>
+axr_status launch(const Q8Attend& a, const Q8Tiles& tl, cudaStream_t st, const char* w) {
+  auto k = q8_prefill_kernel<T, D, I8>;
+  const axr_status rs = ensure_smem(k, PrefillPlan<D>::bytes, w);
+  if (rs != AXR_OK) return rs;
+  k<<<static_cast<unsigned>(tl.tiles * a.Hkv * a.splits), kPfThreads, PrefillPlan<D>::bytes, st>>>(a, tl);
+  if (a.splits > 1)
+    q8_merge_kernel<T, D><<<static_cast<unsigned>(tl.tiles * a.Hkv * kQ8PrefillRows), D, 0, st>>>(a, tl,
+                                                                                                 kQ8PrefillRows);
+  return check_launch(w);
+}
+
+template <typename T>
+axr_status by_d(int d, bool i8, const Q8Attend& a, const Q8Tiles& tl, cudaStream_t st, const char* w) {
+  if (d == 64) return i8 ? launch<T, 64, true>(a, tl, st, w) : launch<T, 64, false>(a, tl, st, w);
+  return i8 ? launch<T, 128, true>(a, tl, st, w) : launch<T, 128, false>(a, tl, st, w);
+}
+
+}  // namespace
+
+axr_status q8_prefill_launch(bool half, int d, bool i8, const Q8Attend& a, const Q8Tiles& tl, cudaStream_t st,
+                             const char* w) {
+  return half ? by_d<__half>(d, i8, a, tl, st, w) : by_d<__nv_bfloat16>(d, i8, a, tl, st, w);
+}
+
+}  // namespace axr
