@@ -31,8 +31,9 @@ Q8Plan plan_decode(int64_t n_tok, int B, int G, int Hkv, int T, bool one, int ma
   return pl;
 }
 
-// The tcgen05 kernel: tiles of 128 rows, two thread blocks per SM, splits of at least two key tiles; a block's set-up
-// (query operand, first code tiles) costs about two key tiles.
+// The tcgen05 kernel: tiles of 256 rows, one thread block per SM.  In units of one key tile (128 tokens), a block's
+// set-up (query operand, first code tiles) costs about 2, and writing and merging the partials of a split axis about 3
+// more: its 256 x d fp32 rows cross HBM twice.
 Q8Plan plan_prefill(int64_t n_tok, int B, int G, int Hkv, int T) {
   Q8Plan pl;
   pl.nrg = kQ8PrefillRows / 8;
@@ -41,8 +42,20 @@ Q8Plan plan_prefill(int64_t n_tok, int B, int G, int Hkv, int T) {
   pl.tl.skip_long = false;
   pl.tl.skip_short = 0;
   pl.tl.tiles = n_tok / pl.tl.tpt + B;
-  const int64_t units = pl.tl.tiles < 65536 ? pl.tl.tiles : 65536;
-  pl.sp = plan_splits(static_cast<int>(units), Hkv, T, 2 * kSmCount, 128, 2, 2.0);
+  const int64_t units = pl.tl.tiles * Hkv;
+  const int64_t total = (static_cast<int64_t>(T) + 127) / 128;
+  pl.sp.splits = 1;
+  pl.sp.chunk = static_cast<int>(total * 128);
+  int64_t best = ((units + kSmCount - 1) / kSmCount) * (total + 2);
+  for (int64_t s = 2; s <= total / 2 && s <= 256; ++s) {
+    const int64_t per = (total + s - 1) / s, splits = (total + per - 1) / per;
+    const int64_t cost = ((units * splits + kSmCount - 1) / kSmCount) * (per + 5);
+    if (cost < best) {
+      best = cost;
+      pl.sp.splits = static_cast<int>(splits);
+      pl.sp.chunk = static_cast<int>(per * 128);
+    }
+  }
   return pl;
 }
 
@@ -119,6 +132,8 @@ extern "C" axr_status axr_q8_attend_paged(const void* q, axr_dtype x_dtype, int6
   int shift = 0;
   axr_status st = check_table(w, block_table, max_blocks, block_tokens, num_blocks, &shift);
   if (st != AXR_OK) return st;
+  if (static_cast<int64_t>(num_blocks) * Hkv * (block_tokens / 16) > 0x7fffffff)
+    return set_error(AXR_EUNSUPPORTED, "%s: the pools have more than 2^31 scale blocks", w);
   if (static_cast<int64_t>(T) > static_cast<int64_t>(max_blocks) * block_tokens)
     return set_error(AXR_EINVAL, "%s: T=%d exceeds max_blocks=%d x block_tokens=%d", w, T, max_blocks, block_tokens);
   if (!std::isfinite(scale)) return set_error(AXR_EINVAL, "%s: scale is not finite", w);

@@ -63,8 +63,8 @@ struct Q8Tiles {
   int skip_short;
 };
 
-// q8_prefill.cu: tiles of up to 128 query rows on the tcgen05 tensor cores, queries and outputs fp16 (half) or bf16.
-constexpr int kQ8PrefillRows = 128;
+// q8_prefill.cu: tiles of up to 256 query rows on the tcgen05 tensor cores, queries and outputs fp16 (half) or bf16.
+constexpr int kQ8PrefillRows = 256;
 axr_status q8_prefill_launch(bool half, int d, bool i8, const Q8Attend& a, const Q8Tiles& tl, cudaStream_t st,
                              const char* w);
 

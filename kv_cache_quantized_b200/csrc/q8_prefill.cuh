@@ -1,23 +1,26 @@
 // Attention of many query tokens over the paged 8-bit cache on the tcgen05 tensor cores.
 //
-// One thread block takes a row tile of up to 128 query rows (tokens x heads of one KV head's group) and a range of the
-// token axis, in key tiles of 128 tokens:
+// One thread block takes up to 256 query rows (tokens x heads of one KV head's group) as two row tiles of 128, and a
+// range of the token axis in key tiles of 128 tokens:
 //   S = Q K^T     M = 128 rows, N = 128 tokens: Q and the key codes in shared memory (fp16, K-major, 128-byte swizzle),
 //                 S in tensor memory, fp32;
 //   P = 2^(ks f S - m), times vs / vref, rounded to fp16 and stored over S in tensor memory;
 //   O += P V      A = P from tensor memory, B = the value codes in shared memory (fp16, N-major: token rows as they
 //                 lie in the cache), O in tensor memory, fp32.
 // Codes turn into fp16 exactly, so the scales of the 16-token blocks never touch the operands: ks goes into the
-// exponent's multiplier and vs onto the weights, one factor for 16 columns.
+// exponent's multiplier and vs, as log2 vs, into its offset, one pair for 16 columns; the normaliser takes vs back out
+// of each 16-column sum.  log2 vs counts relative to lref, the running maximum over tiles rounded up, and not below
+// lref - 60, so that a block of zeros (vs = 0) keeps its place in the normaliser.
 //
-// Warps 0..3 are the softmax (thread = row = tensor-memory lane), warps 4..7 fetch codes two tiles ahead into registers
-// and turn them into fp16 shared-memory operands, warp 8 issues the MMAs.  Two thread blocks share an SM (256 of its 512
-// tensor-memory columns and 97 KB of shared memory each), so that one's MMAs run under the other's softmax.
+// Warps 0..7 are the softmax of the two row tiles (thread = row = tensor-memory lane), warps 8..11 fetch codes a tile
+// ahead into registers and turn them into fp16 operands, two tiles deep, once for both row tiles; warp 12 issues the
+// MMAs, one row tile's under the other's softmax (warps 13..15 only give up registers).
 //
 // Roundings: the weights to fp16 (2^-11; the output is 16-bit), bf16 queries to fp16 after a power of two brought their
 // row's largest magnitude to 2^13..2^14 (exact for coordinates within 2^-27 of it).  The running maximum moves only
 // when it grows by more than 2^kLazy (weights stay below 2^kLazy, and inside fp16 with the 2^(15 - kLazy) they are
-// scaled by), so the output is seldom rescaled.
+// scaled by), so the output is seldom rescaled, and a tile takes one pass over S: the weights are formed with the
+// present maximum and kept in registers until the tile's own maximum is known.
 #pragma once
 
 #include "q8_attend.cuh"
@@ -25,19 +28,19 @@
 
 namespace axr {
 
-constexpr int kPfRows = 128, kPfKeys = 128, kPfThreads = 288;
+constexpr int kPfKeys = 128, kPfThreads = 16 * 32;
 constexpr int kLazy = 6;
-constexpr float kPfUp = static_cast<float>(1 << (15 - kLazy));
 
 template <int D>
 struct PrefillPlan {
-  static constexpr int CB = D / 64;                        // 64-coordinate column blocks of 128-byte rows
-  static constexpr uint32_t BLOCK = 128u * 128u;           // bytes of one column block: 128 rows x 128 bytes
-  static constexpr uint32_t OFF_Q = 0, OFF_K = CB * BLOCK, OFF_V = 2 * CB * BLOCK;
-  static constexpr uint32_t OFF_SC = 3 * CB * BLOCK;       // [2][16] floats: ks, vs of a tile's 8 scale blocks
-  static constexpr uint32_t OFF_BAR = OFF_SC + 2 * 16 * 4;
-  static constexpr size_t bytes = 1024 + OFF_BAR + 64;
-  static constexpr int COLS = 256, COL_S = 0, COL_O = 128; // tensor memory
+  static constexpr uint32_t BLOCK = 128u * 128u;           // a column block: 128 rows x 64 fp16 coordinates (128 bytes)
+  static constexpr uint32_t TILE = D / 64 * BLOCK;         // an operand tile: 128 rows x D
+  static constexpr uint32_t OFF_Q = 0, OFF_K = 2 * TILE, OFF_V = 4 * TILE;  // two row tiles, two stages each
+  static constexpr uint32_t OFF_SC = 6 * TILE;             // [4][32] floats: a key tile's ks[8], off[8], winv[8], lref
+  static constexpr uint32_t OFF_BL = OFF_SC + 4 * 32 * 4;  // [4][8] ints: scale blocks of a tile, by converter warp
+  static constexpr uint32_t OFF_BAR = OFF_BL + 4 * 8 * 4;
+  static constexpr size_t bytes = 1024 + OFF_BAR + 16 * 8;
+  static constexpr uint32_t COLS = 512, COL_S = 0, COL_O = 256;  // tensor memory: S of the row tiles, then O, 128 each
   static constexpr int CH = D / 16;                        // 16-byte code chunks of a row
   static constexpr int NL = kPfKeys * CH / 128;            // chunks a converter thread holds of a tile
 };
@@ -48,25 +51,35 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
-__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
-  unsigned long long rd;
-  asm("mul.rn.f32x2 %0, %1, %2;"
-      : "=l"(rd)
-      : "l"(*reinterpret_cast<unsigned long long*>(&a)), "l"(*reinterpret_cast<unsigned long long*>(&b)));
-  return *reinterpret_cast<float2*>(&rd);
+__device__ __forceinline__ float lg2(float x) {
+  float y;
+  asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
 }
 
-__device__ __forceinline__ void tm_ld32(uint32_t taddr, float (&d)[32]) {
-  uint32_t* u = reinterpret_cast<uint32_t*>(d);
+__device__ __forceinline__ float max3(float a, float b, float c) { return fmaxf(fmaxf(a, b), c); }
+
+// 16 bytes from global memory, or zeros where !on.  Volatile: the loads stay where they are written, a tile ahead.
+__device__ __forceinline__ uint4 load16_if(const uint8_t* p, bool on) {
+  uint4 v;
   asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
-      "%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
-      : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3]), "=r"(u[4]), "=r"(u[5]), "=r"(u[6]), "=r"(u[7]), "=r"(u[8]),
-        "=r"(u[9]), "=r"(u[10]), "=r"(u[11]), "=r"(u[12]), "=r"(u[13]), "=r"(u[14]), "=r"(u[15]), "=r"(u[16]),
-        "=r"(u[17]), "=r"(u[18]), "=r"(u[19]), "=r"(u[20]), "=r"(u[21]), "=r"(u[22]), "=r"(u[23]), "=r"(u[24]),
-        "=r"(u[25]), "=r"(u[26]), "=r"(u[27]), "=r"(u[28]), "=r"(u[29]), "=r"(u[30]), "=r"(u[31])
-      : "r"(taddr)
-      : "memory");
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %5, 0;\n\tmov.b32 %0, 0;\n\tmov.b32 %1, 0;\n\tmov.b32 %2, 0;\n\t"
+      "mov.b32 %3, 0;\n\t@p ld.global.nc.v4.u32 {%0, %1, %2, %3}, [%4];\n\t}"
+      : "=&r"(v.x), "=&r"(v.y), "=&r"(v.z), "=&r"(v.w)
+      : "l"(p), "r"(on ? 1 : 0));
+  return v;
+}
+
+// One lane of a converged warp, the same one every time.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+  return p != 0;
+}
+
+__device__ __forceinline__ uint32_t pack_half2(float a, float b) {
+  const __half2 h = __floats2half2_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&h);
 }
 
 // Shared-memory matrix descriptor with the 128-byte swizzle.
@@ -108,15 +121,17 @@ __device__ __forceinline__ uint32_t sw128(int r, int j) {
 }
 
 template <typename T, int D, bool I8>
-__global__ void __launch_bounds__(kPfThreads, 2)
+__global__ void __launch_bounds__(kPfThreads, 1)
 q8_prefill_kernel(const __grid_constant__ Q8Attend a, const Q8Tiles tl) {
   using P = PrefillPlan<D>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024 - (static_cast<uint32_t>(__cvta_generic_to_shared(smem_raw)) & 1023)) & 1023);
   float* sc = reinterpret_cast<float*>(smem + P::OFF_SC);
   uint64_t* bar = reinterpret_cast<uint64_t*>(smem + P::OFF_BAR);
-  uint64_t *k_full = bar, *v_full = bar + 1, *p_full = bar + 2, *qk_done = bar + 3, *pv_done = bar + 4;
-  uint32_t* tm_slot = reinterpret_cast<uint32_t*>(bar + 5);
+  // by stage: operands written, operands read; by row tile: S written, weights written, output updated
+  uint64_t *k_full = bar, *v_full = bar + 2, *k_free = bar + 4, *v_free = bar + 6;
+  uint64_t *s_full = bar + 8, *p_full = bar + 10, *pv_done = bar + 12;
+  uint32_t* tm_slot = reinterpret_cast<uint32_t*>(bar + 14);
   uint32_t* failed = tm_slot + 1;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
@@ -131,24 +146,30 @@ q8_prefill_kernel(const __grid_constant__ Q8Attend a, const Q8Tiles tl) {
   const Q8Span sp = q8_span(a, b);
   if (!q8_tile_live(a, tl, sp, i0, lane)) return;  // uniform over the block
   const int ntok = min(tl.tpt, sp.count - static_cast<int>(i0)), nrow = ntok * a.G;
+  const int nq = nrow > 128 ? 2 : 1;                             // row tiles in use
   const int first_lim = sp.pos0 + static_cast<int>(i0) + 1;      // keys the tile's first token sees
   const int begin = split * a.chunk, end = min(begin + a.chunk, first_lim + ntok - 1);
   const int n = end > begin ? (end - begin + kPfKeys - 1) / kPfKeys : 0;
 
   // ---- set-up: barriers, tensor memory, the query operand
   if (threadIdx.x == 0) {
-    tc::mbar_init(k_full, 128);
-    tc::mbar_init(v_full, 128);
-    tc::mbar_init(p_full, 128);
-    tc::mbar_init(qk_done, 1);
-    tc::mbar_init(pv_done, 1);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      tc::mbar_init(k_full + i, 128);
+      tc::mbar_init(v_full + i, 128);
+      tc::mbar_init(k_free + i, 1);
+      tc::mbar_init(v_free + i, 1);
+      tc::mbar_init(s_full + i, 1);
+      tc::mbar_init(p_full + i, 128);
+      tc::mbar_init(pv_done + i, 1);
+    }
     *failed = 0;
   }
-  if (warp == 8) tc::tmem_alloc(tm_slot, P::COLS);
+  if (warp == 12) tc::tmem_alloc(tm_slot, P::COLS);
   float f_row = 0.f;
   int lim = 0;
   int64_t orow = 0;
-  if (warp < 4) {
+  if (warp < 8) {
     const int r = threadIdx.x;
     const bool live = r < nrow;
     const int i = static_cast<int>(i0) + (live ? r / a.G : 0), h = hk * a.G + (live ? r % a.G : 0);
@@ -172,16 +193,19 @@ q8_prefill_kernel(const __grid_constant__ Q8Attend a, const Q8Tiles tl) {
     ex = max(-100, min(100, ex - 14));
     const float up = ldexpf(a.mult < 0.f ? -1.f : 1.f, -ex);  // the operand carries the sign, so that f_row >= 0
     f_row = fabsf(a.mult) * ldexpf(1.f, ex);
+    if (warp < 4 * nq) {
 #pragma unroll 4
-    for (int c = 0; c < D / 8; ++c) {
-      Raw8<T> w;
-      float x[8];
-      if (live) w.load(src + 8 * c);
-      else w.zero();
-      w.values(x);
+      for (int c = 0; c < D / 8; ++c) {
+        Raw8<T> w;
+        float x[8];
+        if (live) w.load(src + 8 * c);
+        else w.zero();
+        w.values(x);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) x[e] *= up;
-      store8(reinterpret_cast<__half*>(smem + P::OFF_Q + (c >> 3) * P::BLOCK + sw128(r, c & 7)), x);
+        for (int e = 0; e < 8; ++e) x[e] *= up;
+        store8(reinterpret_cast<__half*>(smem + P::OFF_Q + (r >> 7) * P::TILE + (c >> 3) * P::BLOCK +
+                                         sw128(r & 127, c & 7)), x);
+      }
     }
     tc::fence_async_smem();
   }
@@ -189,17 +213,21 @@ q8_prefill_kernel(const __grid_constant__ Q8Attend a, const Q8Tiles tl) {
   __syncthreads();
   tc::fence_after();
   const uint32_t tm = *tm_slot;
-
-  if (warp >= 4 && warp < 8 && n > 0) {
+  // Registers move from the warpgroup of the MMA warp to the others: 3 x 144 + 72 of the 4 x 128 a thread launched with.
+  if (warp >= 8 && warp < 12) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 144;");
+    if (n > 0) {
     // ---- converters: thread c holds the code chunk (row c / CH + (128 / CH) k, chunk c % CH) of a tile, k < NL
-    const int c = threadIdx.x - 128, chunk = c % P::CH, row_c = c / P::CH;
+    const int c = threadIdx.x - 256, chunk = c % P::CH, row_c = c / P::CH;
     constexpr int RS = 128 / P::CH;                      // rows between two of a thread's chunks (16 or 32)
     const int32_t* table = a.table + static_cast<size_t>(b) * a.max_blocks;
+    const uint8_t* kp = a.kcodes + ((row_c & 15) * D + 16 * chunk);
+    const uint8_t* vp = a.vcodes + ((row_c & 15) * D + 16 * chunk);
     uint4 kw[P::NL], vw[P::NL];
     float ks = 0.f, vs = 0.f;
-    // lane l < 8: pool row of scale block l of a tile, -1 past the end
-    auto rows_of = [&](int j) {
-      int64_t r = -1;
+    // lane l: pool scale block (16 rows) of the tile's block l % 8, -1 past the end
+    auto blocks_of = [&](int j) {
+      int r = -1;
       const int t = begin + j * kPfKeys + 16 * (lane & 7);
       if (t < end) {
         int page = __ldg(table + (t >> a.shift));
@@ -207,201 +235,259 @@ q8_prefill_kernel(const __grid_constant__ Q8Attend a, const Q8Tiles tl) {
           if (lane < 8) atomicOr(a.status, kStatusBadIndex);
           page = 0;
         }
-        r = ((static_cast<int64_t>(page) * a.Hkv + hk) << a.shift) + (t & ((1 << a.shift) - 1));
+        r = ((page * a.Hkv + hk) << (a.shift - 4)) + ((t & ((1 << a.shift) - 1)) >> 4);
       }
       return r;
     };
-    auto fetch = [&](const uint8_t* codes, int64_t rows, uint4 (&w)[P::NL]) {
+    // the blocks' places, from the lanes that hold them to every thread of the warp
+    int* const bl = reinterpret_cast<int*>(smem + P::OFF_BL) + 8 * (warp - 8);
+    auto share = [&](int blocks) {
+      __syncwarp();
+      if (lane < 8) bl[lane] = blocks;
+      __syncwarp();
+    };
+    auto fetch = [&](const uint8_t* codes, uint4 (&w)[P::NL]) {
 #pragma unroll
       for (int k = 0; k < P::NL; ++k) {
-        const int r = row_c + RS * k;
-        const int64_t base = __shfl_sync(0xffffffffu, rows, r >> 4);
-        w[k] = base >= 0 ? __ldg(reinterpret_cast<const uint4*>(codes + (base + (r & 15)) * D) + chunk)
-                         : make_uint4(0, 0, 0, 0);
+        const int blk = bl[(row_c + RS * k) >> 4];
+        w[k] = load16_if(codes + static_cast<int64_t>(blk) * (16 * D), blk >= 0);
       }
     };
-    auto convert = [&](uint32_t off, const uint4 (&w)[P::NL], int valid) {
+    const int odd = (chunk >> 2) & 1;
+    uint8_t* const d0 = smem + (chunk >> 2) * P::BLOCK + sw128(row_c, 2 * (chunk & 3) + odd);
+    uint8_t* const d1 = smem + (chunk >> 2) * P::BLOCK + sw128(row_c, 2 * (chunk & 3) + 1 - odd);
+    auto convert = [&](uint32_t off, uint4 (&w)[P::NL], int valid) {
+      if (valid < kPfKeys) {  // rows no query sees may hold anything (an e4m3 NaN)
+#pragma unroll
+        for (int k = 0; k < P::NL; ++k)
+          if (row_c + RS * k >= valid) w[k] = make_uint4(0, 0, 0, 0);
+      }
 #pragma unroll
       for (int k = 0; k < P::NL; ++k) {
-        const int r = row_c + RS * k;
-        uint4 x = w[k];
-        if (r >= valid) x = make_uint4(0, 0, 0, 0);
-        uint4 lo, hi;
-        q8_halves<I8>(x.x, lo.x, lo.y);
-        q8_halves<I8>(x.y, lo.z, lo.w);
-        q8_halves<I8>(x.z, hi.x, hi.y);
-        q8_halves<I8>(x.w, hi.z, hi.w);
         // 16 coordinates = two 16-byte chunks; the odd column block stores its second chunk first, so that the eight
         // threads of a row hit eight different banks
-        uint8_t* dst = smem + off + (chunk >> 2) * P::BLOCK;
-        const int j0 = 2 * (chunk & 3), odd = (chunk >> 2) & 1;
-        *reinterpret_cast<uint4*>(dst + sw128(r, j0 + odd)) = odd ? hi : lo;
-        *reinterpret_cast<uint4*>(dst + sw128(r, j0 + 1 - odd)) = odd ? lo : hi;
+        uint4 lo, hi;
+        q8_halves<I8>(odd ? w[k].z : w[k].x, lo.x, lo.y);
+        q8_halves<I8>(odd ? w[k].w : w[k].y, lo.z, lo.w);
+        q8_halves<I8>(odd ? w[k].x : w[k].z, hi.x, hi.y);
+        q8_halves<I8>(odd ? w[k].y : w[k].w, hi.z, hi.w);
+        *reinterpret_cast<uint4*>(d0 + off + k * (RS * 128)) = lo;
+        *reinterpret_cast<uint4*>(d1 + off + k * (RS * 128)) = hi;
       }
     };
-    int64_t rows = rows_of(0);
-    fetch(a.kcodes, rows, kw);
-    fetch(a.vcodes, rows, vw);
-    if (rows >= 0) {
-      ks = __ldg(a.kscales + (rows >> 4));
-      vs = __ldg(a.vscales + (rows >> 4));
+    // block table entries run two tiles ahead of the conversion, codes and scales one
+    int next = blocks_of(0), after = n > 1 ? blocks_of(1) : -1;
+    share(next);
+    fetch(kp, kw);
+    fetch(vp, vw);
+    if (next >= 0) {
+      ks = __ldg(a.kscales + next);
+      vs = __ldg(a.vscales + next);
     }
+    float lref = -126.f;
     for (int j = 0; j < n; ++j) {
-      const int valid = end - begin - j * kPfKeys;       // rows of the tile that some query sees
-      const int64_t next = j + 1 < n ? rows_of(j + 1) : -1;
-      if (j > 0 && !warp_wait(qk_done, (j - 1) & 1)) { *failed = 1; break; }
-      convert(P::OFF_K, kw, valid);
-      if (c < 8) {
-        sc[(j & 1) * 16 + c] = ks;
-        sc[(j & 1) * 16 + 8 + c] = vs;
+      const int valid = end - begin - j * kPfKeys, st = j & 1;  // rows of the tile that some query sees
+      const uint32_t ph = ((j >> 1) - 1) & 1;
+      if (j >= 2 && !warp_wait(k_free + st, ph)) { *failed = 1; break; }
+      next = after;
+      after = j + 2 < n ? blocks_of(j + 2) : -1;
+      convert(P::OFF_K + st * P::TILE, kw, valid);
+      if (warp == 8) {
+        float* scj = sc + (j & 3) * 32;
+        const float lv = lg2(vs);
+        float top = lv;
+#pragma unroll
+        for (int x = 4; x > 0; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
+        lref = fmaxf(lref, ceilf(top));
+        const float off = fmaxf(lv, lref - 60.f) - lref + static_cast<float>(15 - kLazy);
+        if (lane < 8) {
+          scj[lane] = ks;
+          scj[8 + lane] = off;
+          scj[16 + lane] = ex2(-off);
+        }
+        if (lane == 0) scj[24] = lref;
       }
       tc::fence_async_smem();
-      tc::mbar_arrive(k_full);
-      ks = vs = 0.f;
-      if (next >= 0) {
-        ks = __ldg(a.kscales + (next >> 4));
-        vs = __ldg(a.vscales + (next >> 4));
-      }
-      fetch(a.kcodes, next, kw);
-      if (j > 0 && !warp_wait(pv_done, (j - 1) & 1)) { *failed = 1; break; }
-      convert(P::OFF_V, vw, valid);
+      tc::mbar_arrive(k_full + st);
+      share(next);
+      fetch(kp, kw);
+      ks = next >= 0 ? __ldg(a.kscales + next) : 0.f;
+      vs = next >= 0 ? __ldg(a.vscales + next) : 0.f;
+      if (j >= 2 && !warp_wait(v_free + st, ph)) { *failed = 1; break; }
+      convert(P::OFF_V + st * P::TILE, vw, valid);
       tc::fence_async_smem();
-      tc::mbar_arrive(v_full);
-      fetch(a.vcodes, next, vw);
+      tc::mbar_arrive(v_full + st);
+      fetch(vp, vw);
     }
-  } else if (warp == 8 && n > 0) {
-    // ---- MMA issue
-    if (lane == 0) {
-      const uint32_t s0 = static_cast<uint32_t>(__cvta_generic_to_shared(smem));
-      for (int j = 0; j < n; ++j) {
-        if (!tc::mbar_wait(k_full, j & 1) || (j > 0 && !tc::mbar_wait(pv_done, (j - 1) & 1))) { *failed = 1; break; }
-        tc::fence_after();
+    }
+  } else if (warp >= 12) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+    if (warp == 12 && n > 0) {
+    // ---- MMA issue: S of both row tiles, then, as each tile's weights arrive, its output and its next S
+    const uint32_t s0 = static_cast<uint32_t>(__cvta_generic_to_shared(smem));
+    auto score = [&](int q, int j) {
+      const uint64_t dq = sw128_desc(s0 + P::OFF_Q + q * P::TILE, 16, 1024);
+      const uint64_t dk = sw128_desc(s0 + P::OFF_K + (j & 1) * P::TILE, 16, 1024);
+      if (elect_one()) {
 #pragma unroll
         for (int s = 0; s < D / 16; ++s) {
-          const uint32_t o = (s >> 2) * P::BLOCK + (s & 3) * 32u;
-          mma_ss(tm + P::COL_S, sw128_desc(s0 + P::OFF_Q + o, 16, 1024), sw128_desc(s0 + P::OFF_K + o, 16, 1024),
-                 pf_idesc(kPfKeys, false), s > 0);
+          const uint32_t o = ((s >> 2) * P::BLOCK + (s & 3) * 32u) >> 4;
+          mma_ss(tm + P::COL_S + 128 * q, dq + o, dk + o, pf_idesc(kPfKeys, false), s > 0);
         }
-        mma_commit(qk_done);
-        if (!tc::mbar_wait(v_full, j & 1) || !tc::mbar_wait(p_full, j & 1)) { *failed = 1; break; }
+        mma_commit(s_full + q);
+        if (q == nq - 1) mma_commit(k_free + (j & 1));
+      }
+      __syncwarp();
+    };
+    bool ok = warp_wait(k_full, 0);
+    tc::fence_after();
+    if (ok)
+      for (int q = 0; q < nq; ++q) score(q, 0);
+    for (int j = 0; j < n && ok; ++j) {
+      ok = warp_wait(v_full + (j & 1), (j >> 1) & 1);
+      const uint64_t dv = sw128_desc(s0 + P::OFF_V + (j & 1) * P::TILE, P::BLOCK, 1024);
+      for (int q = 0; q < nq && ok; ++q) {
+        if (!(ok = warp_wait(p_full + q, j & 1))) break;
         tc::fence_after();
+        if (elect_one()) {
 #pragma unroll
-        for (int s = 0; s < kPfKeys / 16; ++s)
-          mma_ts(tm + P::COL_O, tm + P::COL_S + 8 * s, sw128_desc(s0 + P::OFF_V + s * 2048u, P::BLOCK, 1024),
-                 pf_idesc(D, true), j > 0 || s > 0);
-        mma_commit(pv_done);
+          for (int s = 0; s < kPfKeys / 16; ++s)
+            mma_ts(tm + P::COL_O + 128 * q, tm + P::COL_S + 128 * q + 8 * s, dv + s * (2048u >> 4), pf_idesc(D, true),
+                   j > 0 || s > 0);
+          mma_commit(pv_done + q);
+          if (q == nq - 1) mma_commit(v_free + (j & 1));
+        }
+        __syncwarp();
+        if (j + 1 < n) {  // the next S goes where this tile's weights lie: they must have been read
+          if (!(ok = warp_wait(k_full + ((j + 1) & 1), ((j + 1) >> 1) & 1) && warp_wait(pv_done + q, j & 1))) break;
+          tc::fence_after();
+          score(q, j + 1);
+        }
       }
     }
-  } else if (warp < 4) {
+    if (!ok) *failed = 1;
+    }
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 144;");
+    if (warp < 4 * nq) {
     // ---- softmax: thread = row
-    const uint32_t ts = tm + (static_cast<uint32_t>(warp * 32) << 16) + P::COL_S;
-    const uint32_t to = tm + (static_cast<uint32_t>(warp * 32) << 16) + P::COL_O;
-    float m = -INFINITY, vref = 0.f;
-    float2 l2 = make_float2(0.f, 0.f);
+    const int q = warp >> 2;
+    const uint32_t ts = tm + (static_cast<uint32_t>((warp & 3) * 32) << 16) + P::COL_S + 128 * q;
+    const uint32_t to = tm + (static_cast<uint32_t>((warp & 3) * 32) << 16) + P::COL_O + 128 * q;
+    float m = threadIdx.x < nrow ? -INFINITY : 0.f, l = 0.f, lref = -126.f;  // rows not in use never ask for a second pass
     bool ok = true;
+    // 16 columns of weights from 16 of S: 2^(s cc + off - m), packed to fp16; returns their sum
+    auto weights = [&](const uint32_t (&x)[16], float cc, float off, uint32_t (&w)[8]) {
+      float2 sum = make_float2(0.f, 0.f);
+#pragma unroll
+      for (int e = 0; e < 16; e += 2) {
+        const float2 y = fma2(make_float2(__uint_as_float(x[e]), __uint_as_float(x[e + 1])), make_float2(cc, cc),
+                              make_float2(off, off));
+        const float2 p = make_float2(ex2(y.x), ex2(y.y));
+        sum = add2(sum, p);
+        w[e >> 1] = pack_half2(p.x, p.y);
+      }
+      return sum.x + sum.y;
+    };
     for (int j = 0; j < n; ++j) {
-      if (!warp_wait(qk_done, j & 1)) { ok = false; break; }
+      if (!(ok = warp_wait(s_full + q, j & 1))) break;
       tc::fence_after();
-      const int t0 = begin + j * kPfKeys;
-      const bool masked = t0 + kPfKeys > first_lim || t0 + kPfKeys > end;  // uniform
-      const float* scj = sc + (j & 1) * 16;
-      float cs[8], vmax = 0.f;
+      const float* scj = sc + (j & 3) * 32;
+      const int t1 = begin + (j + 1) * kPfKeys;
+      const bool masked = t1 > first_lim || t1 > end;      // some column is hidden from some row; uniform
+      uint32_t w[8][8];
+      float mx = -INFINITY, lt = 0.f;
+      bool again = masked || scj[24] != lref;              // uniform
+      if (!again) {
+        // one pass: the weights with the maximum so far, the tile's own maximum beside them
+        uint32_t x[2][16];
+        tc::ld_x16(ts, x[0]);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        cs[i] = scj[i] * f_row;
-        vmax = fmaxf(vmax, scj[8 + i]);
-      }
-      const int vis = lim - t0;                            // columns below vis are visible
-      float mx = -INFINITY;
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        float s[32];
-        tm_ld32(ts + 32 * k, s);
-        tc::wait_ld();
-        if (masked) {
-#pragma unroll
-          for (int e = 0; e < 32; ++e) mx = fmaxf(mx, 32 * k + e < vis ? s[e] * cs[2 * k + (e >> 4)] : -INFINITY);
-        } else {
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            float q = s[16 * h];
-#pragma unroll
-            for (int e = 1; e < 16; ++e) q = fmaxf(q, s[16 * h + e]);
-            mx = fmaxf(mx, q * cs[2 * k + h]);
-          }
-        }
-      }
-      // the reference maximum and value scale; the output is rescaled when either moves
-      float alpha = 1.f;
-      if (mx > m + static_cast<float>(kLazy)) {            // m = -inf: any finite maximum
-        alpha = m == -INFINITY ? 0.f : ex2(m - mx);
-        m = mx;
-      }
-      float beta = 1.f;
-      if (vmax > vref) {                                   // uniform
-        const float up = __uint_as_float((__float_as_uint(vmax) + 0x7fffffu) & 0x7f800000u);
-        beta = vref / up;
-        vref = up;
-      }
-      l2.x *= alpha;
-      l2.y *= alpha;
-      alpha *= beta;
-      if (j > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
-        if (!warp_wait(pv_done, (j - 1) & 1)) { ok = false; break; }
-        tc::fence_after();
-#pragma unroll 1
-        for (int k = 0; k < D / 16; ++k) {
-          uint32_t o[16];
-          tc::ld_x16(to + 16 * k, o);
+        for (int k = 0; k < 8; ++k) {
           tc::wait_ld();
+          if (k < 7) tc::ld_x16(ts + 16 * (k + 1), x[(k + 1) & 1]);
+          const float cc = scj[k] * f_row;
+          float y = __uint_as_float(x[k & 1][0]);
 #pragma unroll
-          for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
-          tc::st_x16(to + 16 * k, o);
+          for (int e = 1; e < 15; e += 2) y = max3(y, __uint_as_float(x[k & 1][e]), __uint_as_float(x[k & 1][e + 1]));
+          mx = max3(mx, y * cc, __uint_as_float(x[k & 1][15]) * cc);
+          lt = fmaf(weights(x[k & 1], cc, scj[8 + k] - m, w[k]), scj[16 + k], lt);
         }
+        again = __any_sync(0xffffffffu, !(mx <= m + static_cast<float>(kLazy)));
       }
-      const float mm = m == -INFINITY ? 0.f : m;
-      const float vf = vref > 0.f ? kPfUp / vref : 0.f;
+      if (again) {
+        // the maximum of the visible columns first; the output is rescaled when it, or lref, moves
+        const int vis = lim - (t1 - kPfKeys);              // columns below vis are visible
+        mx = -INFINITY;
+#pragma unroll 1
+        for (int k = 0; k < 8; ++k) {
+          uint32_t x[16];
+          tc::ld_x16(ts + 16 * k, x);
+          tc::wait_ld();
+          const float cc = scj[k] * f_row;
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        float s[32];
-        uint32_t w[16];
-        tm_ld32(ts + 32 * k, s);
-        tc::wait_ld();
+          for (int e = 0; e < 16; ++e)
+            mx = fmaxf(mx, 16 * k + e < vis ? __uint_as_float(x[e]) * cc : -INFINITY);
+        }
+        float alpha = 1.f;
+        if (mx > m + static_cast<float>(kLazy)) {          // m = -inf: any finite maximum
+          alpha = m == -INFINITY ? 0.f : ex2(m - mx);
+          m = mx;
+        }
+        l *= alpha;
+        alpha *= ex2(lref - scj[24]);
+        lref = scj[24];
+        if (j > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
+          if (!(ok = warp_wait(pv_done + q, (j - 1) & 1))) break;
+          tc::fence_after();
+#pragma unroll 1
+          for (int k = 0; k < D / 16; ++k) {
+            uint32_t o[16];
+            tc::ld_x16(to + 16 * k, o);
+            tc::wait_ld();
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const float cc = cs[2 * k + h], vv = scj[8 + 2 * k + h] * vf;
-#pragma unroll
-          for (int e = 0; e < 16; e += 2) {
-            const int col = 16 * h + e;
-            float x0 = fmaf(s[col], cc, -mm), x1 = fmaf(s[col + 1], cc, -mm);
-            if (masked) {
-              x0 = 32 * k + col < vis ? x0 : -INFINITY;
-              x1 = 32 * k + col + 1 < vis ? x1 : -INFINITY;
-            }
-            float2 p = make_float2(ex2(x0), ex2(x1));
-            l2 = add2(l2, p);
-            p = mul2(p, make_float2(vv, vv));
-            const __half2 hp = __floats2half2_rn(p.x, p.y);
-            w[(col) >> 1] = *reinterpret_cast<const uint32_t*>(&hp);
+            for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+            tc::st_x16(to + 16 * k, o);
           }
         }
-        tc::st_x16(ts + 16 * k, w);
+        const float mm = m == -INFINITY ? 0.f : m;
+        lt = 0.f;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          uint32_t x[16];
+          tc::ld_x16(ts + 16 * k, x);
+          tc::wait_ld();
+          const float cc = scj[k] * f_row;
+          // a hidden column becomes -inf, whatever its scale: the multiplier is 1 where it is not positive
+          const float c1 = cc > 0.f ? cc : 1.f, c0 = cc > 0.f ? 1.f : 0.f;
+#pragma unroll
+          for (int e = 0; e < 16; ++e)
+            x[e] = 16 * k + e < vis ? __float_as_uint(__uint_as_float(x[e]) * c0) : 0xff800000u;
+          lt = fmaf(weights(x, c1, scj[8 + k] - mm, w[k]), scj[16 + k], lt);
+        }
+      }
+      l += lt;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        uint32_t y[16];
+#pragma unroll
+        for (int e = 0; e < 16; ++e) y[e] = w[2 * k + (e >> 3)][e & 7];
+        tc::st_x16(ts + 16 * k, y);
       }
       tc::wait_st();
       tc::fence_before();
-      tc::mbar_arrive(p_full);
+      tc::mbar_arrive(p_full + q);
     }
     if (ok && n > 0) {
-      ok = warp_wait(pv_done, (n - 1) & 1);
+      ok = warp_wait(pv_done + q, (n - 1) & 1);
       tc::fence_after();
     }
     if (!ok) *failed = 1;
-    const float l = l2.x + l2.y;
     const bool live = threadIdx.x < nrow;
     const float nan = __uint_as_float(0x7fc00000u);
-    const float unscale = vref * (1.f / kPfUp);
+    const float unscale = ex2(lref - static_cast<float>(15 - kLazy));
     const float f = a.splits == 1 ? (l > 0.f ? unscale / l : 0.f) : unscale;
-    const int64_t part = ((tile * a.Hkv + hk) * kPfRows + threadIdx.x) * a.splits + split;
+    const int64_t part = ((tile * a.Hkv + hk) * kQ8PrefillRows + threadIdx.x) * a.splits + split;
 #pragma unroll 1
     for (int k = 0; k < D / 16; ++k) {
       uint32_t o[16];
@@ -416,14 +502,17 @@ q8_prefill_kernel(const __grid_constant__ Q8Attend a, const Q8Tiles tl) {
         for (int e = 0; e < 16; ++e) x[e] = ok ? 0.f : nan;
       }
       if (live) {
+        float y[2][8];
+#pragma unroll
+        for (int e = 0; e < 16; ++e) y[e >> 3][e & 7] = x[e];
         if (a.splits == 1) {
           T* dst = static_cast<T*>(a.out) + orow * D + 16 * k;
-          store8(dst, *reinterpret_cast<float(*)[8]>(x));
-          store8(dst + 8, *reinterpret_cast<float(*)[8]>(x + 8));
+          store8(dst, y[0]);
+          store8(dst + 8, y[1]);
         } else {
           float* dst = a.ws_o + part * D + 16 * k;
-          store8(dst, *reinterpret_cast<float(*)[8]>(x));
-          store8(dst + 8, *reinterpret_cast<float(*)[8]>(x + 8));
+          store8(dst, y[0]);
+          store8(dst + 8, y[1]);
         }
       }
     }
@@ -431,12 +520,12 @@ q8_prefill_kernel(const __grid_constant__ Q8Attend a, const Q8Tiles tl) {
       a.ws_m[part] = m;
       a.ws_l[part] = ok ? l : nan;
     }
+    }
   }
-  __syncwarp();
   tc::fence_before();
   __syncthreads();
   if (threadIdx.x == 0 && *failed) atomicOr(a.status, 1u);
-  if (warp == 8) {
+  if (warp == 12) {
     tc::fence_after();
     tc::tmem_dealloc(tm, P::COLS);
   }
