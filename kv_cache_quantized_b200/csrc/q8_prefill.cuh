@@ -1,20 +1,22 @@
 // Attention of many query tokens over the paged 8-bit cache on the tcgen05 tensor cores.
 //
 // One thread block takes up to 256 query rows (tokens x heads of one KV head's group) as two row tiles of 128, and a
-// range of the token axis in key tiles of 128 tokens:
-//   S = Q K^T     M = 128 rows, N = 128 tokens: Q and the key codes in shared memory (fp16, K-major, 128-byte swizzle),
-//                 S in tensor memory, fp32;
+// range of the token axis in steps of 64 keys:
+//   S = Q K^T     M = 128 rows, N = 64 tokens: Q and the key codes in shared memory (fp16, K-major, 128-byte swizzle),
+//                 S in tensor memory, fp32, two buffers a row tile;
 //   P = 2^(ks f S - m), times vs / vref, rounded to fp16 and stored over S in tensor memory;
 //   O += P V      A = P from tensor memory, B = the value codes in shared memory (fp16, N-major: token rows as they
 //                 lie in the cache), O in tensor memory, fp32.
+// Steps of 64 keys leave room for the second S: the scores of step i + 1 are there before the softmax of step i is done,
+// and no product waits for another's end (one S of 128 keys a row tile: 1093 us, two of 64: see below).
 // Codes turn into fp16 exactly, so the scales of the 16-token blocks never touch the operands: ks goes into the
 // exponent's multiplier and vs, as log2 vs, into its offset, one pair for 16 columns; the normaliser takes vs back out
 // of each 16-column sum.  log2 vs counts relative to lref, the running maximum over tiles rounded up, and not below
 // lref - 60, so that a block of zeros (vs = 0) keeps its place in the normaliser.
 //
 // Warps 0..7 are the softmax of the two row tiles (thread = row = tensor-memory lane), warps 8..11 fetch codes a tile
-// ahead into registers and turn them into fp16 operands, two tiles deep, once for both row tiles; warp 12 issues the
-// MMAs, one row tile's under the other's softmax (warps 13..15 only give up registers).
+// ahead into registers and turn them into fp16 operands, two tiles deep, once for both row tiles; warps 12 and 13
+// issue the MMAs, one row tile each (warps 14 and 15 only give up registers).
 //
 // Roundings: the weights to fp16 (2^-11; the output is 16-bit), bf16 queries to fp16 after a power of two brought their
 // row's largest magnitude to 2^13..2^14 (exact for coordinates within 2^-27 of it).  The running maximum moves only
@@ -28,7 +30,7 @@
 
 namespace axr {
 
-constexpr int kPfKeys = 128, kPfThreads = 16 * 32;
+constexpr int kPfKeys = 128, kPfStep = 64, kPfThreads = 16 * 32;
 constexpr int kLazy = 6;
 
 template <int D>
@@ -39,7 +41,7 @@ struct PrefillPlan {
   static constexpr uint32_t OFF_SC = 6 * TILE;             // [4][32] floats: a key tile's ks[8], off[8], winv[8], lref
   static constexpr uint32_t OFF_BL = OFF_SC + 4 * 32 * 4;  // [4][8] ints: scale blocks of a tile, by converter warp
   static constexpr uint32_t OFF_BAR = OFF_BL + 4 * 8 * 4;
-  static constexpr size_t bytes = 1024 + OFF_BAR + 16 * 8;
+  static constexpr size_t bytes = 1024 + OFF_BAR + 22 * 8;
   static constexpr uint32_t COLS = 512, COL_S = 0, COL_O = 256;  // tensor memory: S of the row tiles, then O, 128 each
   static constexpr int CH = D / 16;                        // 16-byte code chunks of a row
   static constexpr int NL = kPfKeys * CH / 128;            // chunks a converter thread holds of a tile
@@ -128,10 +130,10 @@ q8_prefill_kernel(const __grid_constant__ Q8Attend a, const Q8Tiles tl) {
   uint8_t* smem = smem_raw + ((1024 - (static_cast<uint32_t>(__cvta_generic_to_shared(smem_raw)) & 1023)) & 1023);
   float* sc = reinterpret_cast<float*>(smem + P::OFF_SC);
   uint64_t* bar = reinterpret_cast<uint64_t*>(smem + P::OFF_BAR);
-  // by stage: operands written, operands read; by row tile: S written, weights written, output updated
+  // by stage: operands written, operands read; by row tile and S buffer: S written, weights written, output updated
   uint64_t *k_full = bar, *v_full = bar + 2, *k_free = bar + 4, *v_free = bar + 6;
-  uint64_t *s_full = bar + 8, *p_full = bar + 10, *pv_done = bar + 12;
-  uint32_t* tm_slot = reinterpret_cast<uint32_t*>(bar + 14);
+  uint64_t *s_full = bar + 8, *p_full = bar + 12, *pv_done = bar + 16;  // [row tile][S buffer]
+  uint32_t* tm_slot = reinterpret_cast<uint32_t*>(bar + 20);
   uint32_t* failed = tm_slot + 1;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
@@ -149,7 +151,8 @@ q8_prefill_kernel(const __grid_constant__ Q8Attend a, const Q8Tiles tl) {
   const int nq = nrow > 128 ? 2 : 1;                             // row tiles in use
   const int first_lim = sp.pos0 + static_cast<int>(i0) + 1;      // keys the tile's first token sees
   const int begin = split * a.chunk, end = min(begin + a.chunk, first_lim + ntok - 1);
-  const int n = end > begin ? (end - begin + kPfKeys - 1) / kPfKeys : 0;
+  const int n = end > begin ? (end - begin + kPfKeys - 1) / kPfKeys : 0;  // operand stages
+  const int ns = end > begin ? (end - begin + kPfStep - 1) / kPfStep : 0;  // steps
 
   // ---- set-up: barriers, tensor memory, the query operand
   if (threadIdx.x == 0) {
@@ -157,8 +160,11 @@ q8_prefill_kernel(const __grid_constant__ Q8Attend a, const Q8Tiles tl) {
     for (int i = 0; i < 2; ++i) {
       tc::mbar_init(k_full + i, 128);
       tc::mbar_init(v_full + i, 128);
-      tc::mbar_init(k_free + i, 1);
-      tc::mbar_init(v_free + i, 1);
+      tc::mbar_init(k_free + i, nq);
+      tc::mbar_init(v_free + i, nq);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
       tc::mbar_init(s_full + i, 1);
       tc::mbar_init(p_full + i, 128);
       tc::mbar_init(pv_done + i, 1);
@@ -322,47 +328,49 @@ q8_prefill_kernel(const __grid_constant__ Q8Attend a, const Q8Tiles tl) {
     }
   } else if (warp >= 12) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
-    if (warp == 12 && n > 0) {
-    // ---- MMA issue: S of both row tiles, then, as each tile's weights arrive, its output and its next S
+    if (warp < 12 + nq && ns > 0) {
+    // ---- MMA issue, one warp a row tile.  Step i uses S buffer i % 2: its S may be written once the weights of step
+    // i - 2, which lie there, have been read (pv_done).
+    const int q = warp - 12;
     const uint32_t s0 = static_cast<uint32_t>(__cvta_generic_to_shared(smem));
-    auto score = [&](int q, int j) {
-      const uint64_t dq = sw128_desc(s0 + P::OFF_Q + q * P::TILE, 16, 1024);
-      const uint64_t dk = sw128_desc(s0 + P::OFF_K + (j & 1) * P::TILE, 16, 1024);
+    const uint64_t dq = sw128_desc(s0 + P::OFF_Q + q * P::TILE, 16, 1024);
+    auto score = [&](int i) {
+      const uint64_t dk = sw128_desc(s0 + P::OFF_K + ((i >> 1) & 1) * P::TILE + (i & 1) * (kPfStep * 128), 16, 1024);
       if (elect_one()) {
 #pragma unroll
         for (int s = 0; s < D / 16; ++s) {
           const uint32_t o = ((s >> 2) * P::BLOCK + (s & 3) * 32u) >> 4;
-          mma_ss(tm + P::COL_S + 128 * q, dq + o, dk + o, pf_idesc(kPfKeys, false), s > 0);
+          mma_ss(tm + P::COL_S + 128 * q + kPfStep * (i & 1), dq + o, dk + o, pf_idesc(kPfStep, false), s > 0);
         }
-        mma_commit(s_full + q);
-        if (q == nq - 1) mma_commit(k_free + (j & 1));
+        mma_commit(s_full + 2 * q + (i & 1));
+        if (i & 1) mma_commit(k_free + ((i >> 1) & 1));
       }
       __syncwarp();
     };
     bool ok = warp_wait(k_full, 0);
     tc::fence_after();
     if (ok)
-      for (int q = 0; q < nq; ++q) score(q, 0);
-    for (int j = 0; j < n && ok; ++j) {
-      ok = warp_wait(v_full + (j & 1), (j >> 1) & 1);
-      const uint64_t dv = sw128_desc(s0 + P::OFF_V + (j & 1) * P::TILE, P::BLOCK, 1024);
-      for (int q = 0; q < nq && ok; ++q) {
-        if (!(ok = warp_wait(p_full + q, j & 1))) break;
-        tc::fence_after();
-        if (elect_one()) {
+      for (int i = 0; i < 2 && i < ns; ++i) score(i);
+    for (int i = 0; i < ns && ok; ++i) {
+      const int st = (i >> 1) & 1;
+      if (!(i & 1) && !(ok = warp_wait(v_full + st, (i >> 2) & 1))) break;
+      if (!(ok = warp_wait(p_full + 2 * q + (i & 1), (i >> 1) & 1))) break;
+      tc::fence_after();
+      const uint64_t dv = sw128_desc(s0 + P::OFF_V + st * P::TILE + (i & 1) * (kPfStep * 128), P::BLOCK, 1024);
+      if (elect_one()) {
 #pragma unroll
-          for (int s = 0; s < kPfKeys / 16; ++s)
-            mma_ts(tm + P::COL_O + 128 * q, tm + P::COL_S + 128 * q + 8 * s, dv + s * (2048u >> 4), pf_idesc(D, true),
-                   j > 0 || s > 0);
-          mma_commit(pv_done + q);
-          if (q == nq - 1) mma_commit(v_free + (j & 1));
-        }
-        __syncwarp();
-        if (j + 1 < n) {  // the next S goes where this tile's weights lie: they must have been read
-          if (!(ok = warp_wait(k_full + ((j + 1) & 1), ((j + 1) >> 1) & 1) && warp_wait(pv_done + q, j & 1))) break;
-          tc::fence_after();
-          score(q, j + 1);
-        }
+        for (int s = 0; s < kPfStep / 16; ++s)
+          mma_ts(tm + P::COL_O + 128 * q, tm + P::COL_S + 128 * q + kPfStep * (i & 1) + 8 * s, dv + s * (2048u >> 4),
+                 pf_idesc(D, true), i > 0 || s > 0);
+        mma_commit(pv_done + 2 * q + (i & 1));
+        if (i & 1) mma_commit(v_free + st);
+      }
+      __syncwarp();
+      if (i + 2 < ns) {
+        if (!(i & 1) && !(ok = warp_wait(k_full + (((i + 2) >> 1) & 1), ((i + 2) >> 2) & 1))) break;
+        if (!(ok = warp_wait(pv_done + 2 * q + (i & 1), (i >> 1) & 1))) break;
+        tc::fence_after();
+        score(i + 2);
       }
     }
     if (!ok) *failed = 1;
@@ -372,7 +380,7 @@ q8_prefill_kernel(const __grid_constant__ Q8Attend a, const Q8Tiles tl) {
     if (warp < 4 * nq) {
     // ---- softmax: thread = row
     const int q = warp >> 2;
-    const uint32_t ts = tm + (static_cast<uint32_t>((warp & 3) * 32) << 16) + P::COL_S + 128 * q;
+    const uint32_t tq = tm + (static_cast<uint32_t>((warp & 3) * 32) << 16) + P::COL_S + 128 * q;
     const uint32_t to = tm + (static_cast<uint32_t>((warp & 3) * 32) << 16) + P::COL_O + 128 * q;
     float m = threadIdx.x < nrow ? -INFINITY : 0.f, l = 0.f, lref = -126.f;  // rows not in use never ask for a second pass
     bool ok = true;
@@ -389,23 +397,25 @@ q8_prefill_kernel(const __grid_constant__ Q8Attend a, const Q8Tiles tl) {
       }
       return sum.x + sum.y;
     };
-    for (int j = 0; j < n; ++j) {
-      if (!(ok = warp_wait(s_full + q, j & 1))) break;
+    for (int i = 0; i < ns; ++i) {
+      if (!(ok = warp_wait(s_full + 2 * q + (i & 1), (i >> 1) & 1))) break;
       tc::fence_after();
-      const float* scj = sc + (j & 3) * 32;
-      const int t1 = begin + (j + 1) * kPfKeys;
+      const float* scj = sc + ((i >> 1) & 3) * 32 + (i & 1) * (kPfStep / 16);  // the step's ks; off and winv 8 and 16 on
+      const float top = sc[((i >> 1) & 3) * 32 + 24];
+      const uint32_t ts = tq + kPfStep * (i & 1);
+      const int t1 = begin + (i + 1) * kPfStep;
       const bool masked = t1 > first_lim || t1 > end;      // some column is hidden from some row; uniform
-      uint32_t w[8][8];
+      uint32_t w[kPfStep / 16][8];
       float mx = -INFINITY, lt = 0.f;
-      bool again = masked || scj[24] != lref;              // uniform
+      bool again = masked || top != lref;              // uniform
       if (!again) {
         // one pass: the weights with the maximum so far, the tile's own maximum beside them
         uint32_t x[2][16];
         tc::ld_x16(ts, x[0]);
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
+        for (int k = 0; k < kPfStep / 16; ++k) {
           tc::wait_ld();
-          if (k < 7) tc::ld_x16(ts + 16 * (k + 1), x[(k + 1) & 1]);
+          if (k + 1 < kPfStep / 16) tc::ld_x16(ts + 16 * (k + 1), x[(k + 1) & 1]);
           const float cc = scj[k] * f_row;
           float y = __uint_as_float(x[k & 1][0]);
 #pragma unroll
@@ -417,10 +427,10 @@ q8_prefill_kernel(const __grid_constant__ Q8Attend a, const Q8Tiles tl) {
       }
       if (again) {
         // the maximum of the visible columns first; the output is rescaled when it, or lref, moves
-        const int vis = lim - (t1 - kPfKeys);              // columns below vis are visible
+        const int vis = lim - (t1 - kPfStep);              // columns below vis are visible
         mx = -INFINITY;
 #pragma unroll 1
-        for (int k = 0; k < 8; ++k) {
+        for (int k = 0; k < kPfStep / 16; ++k) {
           uint32_t x[16];
           tc::ld_x16(ts + 16 * k, x);
           tc::wait_ld();
@@ -435,10 +445,10 @@ q8_prefill_kernel(const __grid_constant__ Q8Attend a, const Q8Tiles tl) {
           m = mx;
         }
         l *= alpha;
-        alpha *= ex2(lref - scj[24]);
-        lref = scj[24];
-        if (j > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
-          if (!(ok = warp_wait(pv_done + q, (j - 1) & 1))) break;
+        alpha *= ex2(lref - top);
+        lref = top;
+        if (i > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
+          if (!(ok = warp_wait(pv_done + 2 * q + ((i - 1) & 1), ((i - 1) >> 1) & 1))) break;
           tc::fence_after();
 #pragma unroll 1
           for (int k = 0; k < D / 16; ++k) {
@@ -453,7 +463,7 @@ q8_prefill_kernel(const __grid_constant__ Q8Attend a, const Q8Tiles tl) {
         const float mm = m == -INFINITY ? 0.f : m;
         lt = 0.f;
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
+        for (int k = 0; k < kPfStep / 16; ++k) {
           uint32_t x[16];
           tc::ld_x16(ts + 16 * k, x);
           tc::wait_ld();
@@ -468,7 +478,7 @@ q8_prefill_kernel(const __grid_constant__ Q8Attend a, const Q8Tiles tl) {
       }
       l += lt;
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
+      for (int k = 0; k < kPfStep / 32; ++k) {
         uint32_t y[16];
 #pragma unroll
         for (int e = 0; e < 16; ++e) y[e] = w[2 * k + (e >> 3)][e & 7];
@@ -476,10 +486,10 @@ q8_prefill_kernel(const __grid_constant__ Q8Attend a, const Q8Tiles tl) {
       }
       tc::wait_st();
       tc::fence_before();
-      tc::mbar_arrive(p_full + q);
+      tc::mbar_arrive(p_full + 2 * q + (i & 1));
     }
-    if (ok && n > 0) {
-      ok = warp_wait(pv_done + q, (n - 1) & 1);
+    if (ok && ns > 0) {
+      ok = warp_wait(pv_done + 2 * q + ((ns - 1) & 1), ((ns - 1) >> 1) & 1);
       tc::fence_after();
     }
     if (!ok) *failed = 1;
