@@ -15,8 +15,8 @@
 // lref - 60, so that a block of zeros (vs = 0) keeps its place in the normaliser.
 //
 // Warps 0..7 are the softmax of the two row tiles (thread = row = tensor-memory lane), warps 8..11 fetch codes a tile
-// ahead into registers and turn them into fp16 operands, two tiles deep, once for both row tiles; warps 12 and 13
-// issue the MMAs, one row tile each (warps 14 and 15 only give up registers).
+// ahead into registers and turn them into fp16 operands, two tiles deep, once for both row tiles; warps 12..15 issue
+// the MMAs of S and of O, one product of one row tile each.
 //
 // Roundings: the weights to fp16 (2^-11; the output is 16-bit), bf16 queries to fp16 after a power of two brought their
 // row's largest magnitude to 2^13..2^14 (exact for coordinates within 2^-27 of it).  The running maximum moves only
@@ -112,9 +112,18 @@ __device__ __forceinline__ void mma_commit(uint64_t* mbar) {
   asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(mb) : "memory");
 }
 
-// A bounded wait whose outcome is the same for the whole warp.
+// A bounded wait whose outcome is the same for the whole warp.  Each poll may sleep in hardware for up to a millisecond,
+// so that waiting warps leave the issue slots and the shared-memory pipe to the working ones; about two seconds in all.
 __device__ __forceinline__ bool warp_wait(uint64_t* mbar, uint32_t parity) {
-  return __all_sync(0xffffffffu, tc::mbar_wait(mbar, parity));
+  const uint32_t mb = static_cast<uint32_t>(__cvta_generic_to_shared(mbar));
+  uint32_t done = 0;
+  for (int it = 0; it < 2000 && !done; ++it)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(done)
+        : "r"(mb), "r"(parity), "r"(1000000u)
+        : "memory");
+  return __all_sync(0xffffffffu, done != 0);
 }
 
 // Byte offset of the 16-byte chunk j (0..7) of row r in a column block.
@@ -219,9 +228,7 @@ q8_prefill_kernel(const __grid_constant__ Q8Attend a, const Q8Tiles tl) {
   __syncthreads();
   tc::fence_after();
   const uint32_t tm = *tm_slot;
-  // Registers move from the warpgroup of the MMA warp to the others: 3 x 144 + 72 of the 4 x 128 a thread launched with.
   if (warp >= 8 && warp < 12) {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 144;");
     if (n > 0) {
     // ---- converters: thread c holds the code chunk (row c / CH + (128 / CH) k, chunk c % CH) of a tile, k < NL
     const int c = threadIdx.x - 256, chunk = c % P::CH, row_c = c / P::CH;
@@ -327,56 +334,51 @@ q8_prefill_kernel(const __grid_constant__ Q8Attend a, const Q8Tiles tl) {
     }
     }
   } else if (warp >= 12) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
-    if (warp < 12 + nq && ns > 0) {
-    // ---- MMA issue, one warp a row tile.  Step i uses S buffer i % 2: its S may be written once the weights of step
-    // i - 2, which lie there, have been read (pv_done).
-    const int q = warp - 12;
+    // ---- MMA issue: warps 12 and 13 form S of row tiles 0 and 1, warps 14 and 15 their O.  Step i uses S buffer i % 2:
+    // its S may be written once the weights of step i - 2, which lie there, have been read (pv_done).  A satisfied wait
+    // costs its warp about 170 clocks, so the four chains run side by side and the tensor pipe always has work queued.
+    const int q = warp & 1;
     const uint32_t s0 = static_cast<uint32_t>(__cvta_generic_to_shared(smem));
-    const uint64_t dq = sw128_desc(s0 + P::OFF_Q + q * P::TILE, 16, 1024);
-    auto score = [&](int i) {
-      const uint64_t dk = sw128_desc(s0 + P::OFF_K + ((i >> 1) & 1) * P::TILE + (i & 1) * (kPfStep * 128), 16, 1024);
-      if (elect_one()) {
-#pragma unroll
-        for (int s = 0; s < D / 16; ++s) {
-          const uint32_t o = ((s >> 2) * P::BLOCK + (s & 3) * 32u) >> 4;
-          mma_ss(tm + P::COL_S + 128 * q + kPfStep * (i & 1), dq + o, dk + o, pf_idesc(kPfStep, false), s > 0);
-        }
-        mma_commit(s_full + 2 * q + (i & 1));
-        if (i & 1) mma_commit(k_free + ((i >> 1) & 1));
-      }
-      __syncwarp();
-    };
-    bool ok = warp_wait(k_full, 0);
-    tc::fence_after();
-    if (ok)
-      for (int i = 0; i < 2 && i < ns; ++i) score(i);
-    for (int i = 0; i < ns && ok; ++i) {
-      const int st = (i >> 1) & 1;
-      if (!(i & 1) && !(ok = warp_wait(v_full + st, (i >> 2) & 1))) break;
-      if (!(ok = warp_wait(p_full + 2 * q + (i & 1), (i >> 1) & 1))) break;
-      tc::fence_after();
-      const uint64_t dv = sw128_desc(s0 + P::OFF_V + st * P::TILE + (i & 1) * (kPfStep * 128), P::BLOCK, 1024);
-      if (elect_one()) {
-#pragma unroll
-        for (int s = 0; s < kPfStep / 16; ++s)
-          mma_ts(tm + P::COL_O + 128 * q, tm + P::COL_S + 128 * q + kPfStep * (i & 1) + 8 * s, dv + s * (2048u >> 4),
-                 pf_idesc(D, true), i > 0 || s > 0);
-        mma_commit(pv_done + 2 * q + (i & 1));
-        if (i & 1) mma_commit(v_free + st);
-      }
-      __syncwarp();
-      if (i + 2 < ns) {
-        if (!(i & 1) && !(ok = warp_wait(k_full + (((i + 2) >> 1) & 1), ((i + 2) >> 2) & 1))) break;
-        if (!(ok = warp_wait(pv_done + 2 * q + (i & 1), (i >> 1) & 1))) break;
+    bool ok = true;
+    if (q < nq && warp < 14) {
+      const uint64_t dq = sw128_desc(s0 + P::OFF_Q + q * P::TILE, 16, 1024);
+      for (int i = 0; i < ns; ++i) {
+        const int st = (i >> 1) & 1;
+        if (!(i & 1) && !(ok = warp_wait(k_full + st, (i >> 2) & 1))) break;
+        if (i >= 2 && !(ok = warp_wait(pv_done + 2 * q + (i & 1), ((i >> 1) - 1) & 1))) break;
         tc::fence_after();
-        score(i + 2);
+        const uint64_t dk = sw128_desc(s0 + P::OFF_K + st * P::TILE + (i & 1) * (kPfStep * 128), 16, 1024);
+        if (elect_one()) {
+#pragma unroll
+          for (int s = 0; s < D / 16; ++s) {
+            const uint32_t o = ((s >> 2) * P::BLOCK + (s & 3) * 32u) >> 4;
+            mma_ss(tm + P::COL_S + 128 * q + kPfStep * (i & 1), dq + o, dk + o, pf_idesc(kPfStep, false), s > 0);
+          }
+          mma_commit(s_full + 2 * q + (i & 1));
+          if (i & 1) mma_commit(k_free + st);
+        }
+        __syncwarp();
+      }
+    } else if (q < nq) {
+      for (int i = 0; i < ns; ++i) {
+        const int st = (i >> 1) & 1;
+        if (!(i & 1) && !(ok = warp_wait(v_full + st, (i >> 2) & 1))) break;
+        if (!(ok = warp_wait(p_full + 2 * q + (i & 1), (i >> 1) & 1))) break;
+        tc::fence_after();
+        const uint64_t dv = sw128_desc(s0 + P::OFF_V + st * P::TILE + (i & 1) * (kPfStep * 128), P::BLOCK, 1024);
+        if (elect_one()) {
+#pragma unroll
+          for (int s = 0; s < kPfStep / 16; ++s)
+            mma_ts(tm + P::COL_O + 128 * q, tm + P::COL_S + 128 * q + kPfStep * (i & 1) + 8 * s, dv + s * (2048u >> 4),
+                   pf_idesc(D, true), i > 0 || s > 0);
+          mma_commit(pv_done + 2 * q + (i & 1));
+          if (i & 1) mma_commit(v_free + st);
+        }
+        __syncwarp();
       }
     }
     if (!ok) *failed = 1;
-    }
   } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 144;");
     if (warp < 4 * nq) {
     // ---- softmax: thread = row
     const int q = warp >> 2;
