@@ -40,6 +40,21 @@ axr_status encode_cache_map(CUtensorMap* map, const void* base, size_t rows, int
   return AXR_OK;
 }
 
+axr_status encode_byte_map(CUtensorMap* map, const void* base, size_t rows, int D, int box_rows, const char* what) {
+  auto fn = encode_fn();
+  if (!fn) return set_error(AXR_ECUDA, "%s: cuTensorMapEncodeTiled unavailable", what);
+  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(rows)};
+  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(D)};
+  const cuuint32_t box[2] = {static_cast<cuuint32_t>(D), static_cast<cuuint32_t>(box_rows)};
+  const cuuint32_t estr[2] = {1u, 1u};
+  const CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, estr,
+                        CU_TENSOR_MAP_INTERLEAVE_NONE,
+                        D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                        CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return set_error(AXR_ECUDA, "%s: cuTensorMapEncodeTiled failed (%d)", what, (int)r);
+  return AXR_OK;
+}
+
 namespace {
 
 template <int D, int G>

@@ -49,6 +49,10 @@ axr_status attend_partial_launch(int d, int bits, int G, bool vq, const DecodeAr
 // (dense.cu).
 axr_status encode_cache_map(CUtensorMap* map, const void* base, size_t rows, int D, int box_rows, const char* what);
 
+// 2-D TMA map over 8-bit rows [rows, D], D = 64 or 128: boxes of `box_rows` whole rows, swizzled over their D bytes
+// (dense.cu).
+axr_status encode_byte_map(CUtensorMap* map, const void* base, size_t rows, int D, int box_rows, const char* what);
+
 // Quantized keys over fp16 (vq false) or quantized row-layout values on contiguous caches, as a stream of per-warp
 // workers (attend_stream.cu); decode steps included.  Code rows of whole 16-byte chunks, or an even capacity
 // (attend_stream_supported); the arguments carry the plan_splits_stream split plan for its worker count.

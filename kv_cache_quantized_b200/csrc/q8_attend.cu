@@ -3,21 +3,21 @@
 
 #include "axr_host.h"
 #include "paged_host.h"
-#include "q8_decode.cuh"
+#include "q8_attend.cuh"
 
 namespace axr {
 namespace {
 
-constexpr int kDecodeThreads = 128;
-constexpr int kDecodeWorkers = kSmCount * 8;
-
-// Row groups of 8 and tiles of a call.
+// Kernel and workspace of a call.
 struct Q8Plan {
   Q8Tiles tl;
-  int nrg;
-  SplitPlan sp;
+  int nrg;        // row groups of 8 of a tile
+  int grid;       // q8_decode: thread blocks
+  SplitPlan sp;   // q8_prefill
+  size_t parts;   // partial rows in the workspace
 };
 
+// The warp-MMA kernel: one block per SM, fewer when shares of four key tiles would not fill them.
 Q8Plan plan_decode(int64_t n_tok, int B, int G, int Hkv, int T, bool one, int max_q) {
   Q8Plan pl;
   pl.nrg = (one ? static_cast<int64_t>(max_q) * G <= 8 : G <= 8 && n_tok <= B) ? 1 : 2;
@@ -26,8 +26,11 @@ Q8Plan plan_decode(int64_t n_tok, int B, int G, int Hkv, int T, bool one, int ma
   pl.tl.skip_long = false;
   pl.tl.skip_short = 0;
   pl.tl.tiles = one ? B : n_tok / pl.tl.tpt + B;
-  const int64_t units = pl.tl.tiles < 65536 ? pl.tl.tiles : 65536;
-  pl.sp = plan_splits(static_cast<int>(units), Hkv, T, kDecodeWorkers, 32, 2, 2.0);
+  pl.sp.splits = 1;
+  pl.sp.chunk = 0;
+  const int64_t shares = (pl.tl.tiles * Hkv * ((static_cast<int64_t>(T) + 31) / 32) + 3) / 4;
+  pl.grid = static_cast<int>(shares < 1 ? 1 : shares < kSmCount ? shares : kSmCount);
+  pl.parts = static_cast<size_t>(pl.grid) * kQ8DecodeWarps * 2 * 8 * pl.nrg;
   return pl;
 }
 
@@ -56,37 +59,13 @@ Q8Plan plan_prefill(int64_t n_tok, int B, int G, int Hkv, int T) {
       pl.sp.chunk = static_cast<int>(per * 128);
     }
   }
+  pl.grid = 0;
+  pl.parts = pl.sp.splits == 1 ? 0 : static_cast<size_t>(pl.tl.tiles) * Hkv * kQ8PrefillRows * pl.sp.splits;
   return pl;
 }
 
-size_t partial_bytes(const Q8Plan& pl, int Hkv, int d) {
-  if (pl.sp.splits == 1) return 0;
-  const size_t parts = static_cast<size_t>(pl.tl.tiles) * Hkv * 8 * pl.nrg * pl.sp.splits;
-  return (parts * (static_cast<size_t>(d) + 2) * sizeof(float) + 255) / 256 * 256;
-}
-
-template <typename T, int D, bool I8, int NRG>
-axr_status launch(const Q8Attend& a, const Q8Plan& pl, cudaStream_t st, const char* w) {
-  const int64_t items = pl.tl.tiles * a.Hkv * a.splits;
-  const int per = kDecodeThreads / 32;
-  int64_t grid = (items + per - 1) / per;
-  if (grid > kSmCount * 4) grid = kSmCount * 4;
-  q8_decode_kernel<T, D, I8, NRG><<<static_cast<unsigned>(grid), kDecodeThreads, 0, st>>>(a, pl.tl);
-  if (a.splits > 1)
-    q8_merge_kernel<T, D><<<static_cast<unsigned>(pl.tl.tiles * a.Hkv * 8 * NRG), D, 0, st>>>(a, pl.tl, 8 * NRG);
-  return check_launch(w);
-}
-
-template <typename T, int D, bool I8>
-axr_status by_rows(const Q8Attend& a, const Q8Plan& pl, cudaStream_t st, const char* w) {
-  return pl.nrg == 1 ? launch<T, D, I8, 1>(a, pl, st, w) : launch<T, D, I8, 2>(a, pl, st, w);
-}
-
-template <typename T>
-axr_status by_kind(int d, int kind, const Q8Attend& a, const Q8Plan& pl, cudaStream_t st, const char* w) {
-  const bool i8 = kind == AXR_Q8_INT;
-  if (d == 64) return i8 ? by_rows<T, 64, true>(a, pl, st, w) : by_rows<T, 64, false>(a, pl, st, w);
-  return i8 ? by_rows<T, 128, true>(a, pl, st, w) : by_rows<T, 128, false>(a, pl, st, w);
+size_t partial_bytes(const Q8Plan& pl, int d) {
+  return (pl.parts * (static_cast<size_t>(d) + 2) * sizeof(float) + 255) / 256 * 256;
 }
 
 bool one_tile(bool ragged, int max_q, int G) { return !ragged || (max_q > 0 && static_cast<int64_t>(max_q) * G <= 16); }
@@ -102,8 +81,8 @@ extern "C" size_t axr_q8_attend_workspace_bytes(int64_t n_tok, int max_q, int B,
   const int G = Hq / Hkv;
   if (max_q == 0 || max_q > n_tok) max_q = static_cast<int>(n_tok);
   const bool one = one_tile(true, max_q, G);
-  const size_t x = partial_bytes(plan_decode(n_tok, B, G, Hkv, T, one, max_q), Hkv, d);
-  const size_t y = one ? 0 : partial_bytes(plan_prefill(n_tok, B, G, Hkv, T), Hkv, d);
+  const size_t x = partial_bytes(plan_decode(n_tok, B, G, Hkv, T, one, max_q), d);
+  const size_t y = one ? 0 : partial_bytes(plan_prefill(n_tok, B, G, Hkv, T), d);
   return x > y ? x : y;
 }
 
@@ -160,21 +139,18 @@ extern "C" axr_status axr_q8_attend_paged(const void* q, axr_dtype x_dtype, int6
   if (pl.tl.tiles * Hkv * 8 * pl.nrg > 0x7fffffff || pl.tl.tiles * Hkv * pl.sp.splits > 0x7fffffff) return set_error(AXR_EUNSUPPORTED, "%s: too many rows", w);
   a.splits = pl.sp.splits;
   a.chunk = pl.sp.chunk;
-  const size_t need = partial_bytes(pl, Hkv, d);
+  const size_t need = partial_bytes(pl, d);
   if (need) {
     if (!workspace || ws_bytes < need)
       return set_error(AXR_EWORKSPACE, "%s: workspace of %zu bytes, need %zu", w, workspace ? ws_bytes : 0, need);
     if (!aligned(workspace, 16)) return set_error(AXR_EINVAL, "%s: workspace not 16-byte aligned", w);
-    const size_t parts = static_cast<size_t>(pl.tl.tiles) * Hkv * 8 * pl.nrg * a.splits;
     a.ws_o = static_cast<float*>(workspace);
-    a.ws_m = a.ws_o + parts * d;
-    a.ws_l = a.ws_m + parts;
+    a.ws_m = a.ws_o + pl.parts * d;
+    a.ws_l = a.ws_m + pl.parts;
   }
   a.status = status_word();
   if (!a.status) return set_error(AXR_ECUDA, "%s: the status word has no device address", w);
   cudaStream_t s = as_stream(stream);
   if (prefill) return q8_prefill_launch(x_dtype == AXR_F16, d, kind == AXR_Q8_INT, a, pl.tl, s, w);
-  if (x_dtype == AXR_F16) return by_kind<__half>(d, kind, a, pl, s, w);
-  if (x_dtype == AXR_BF16) return by_kind<__nv_bfloat16>(d, kind, a, pl, s, w);
-  return by_kind<float>(d, kind, a, pl, s, w);
+  return q8_decode_launch(x_dtype, d, kind == AXR_Q8_INT, pl.nrg, pl.grid, a, pl.tl, s, w);
 }

@@ -21,10 +21,10 @@ struct Q8Attend {
   const int32_t* cu;        // [B + 1] or null: one query token per sequence
   const int32_t* seq_lens;  // [B] or null: T
   void* out;                // [n_tok, Hq, D]
-  float *ws_o, *ws_m, *ws_l;  // [tiles, Hkv, rows, splits, D], [tiles, Hkv, rows, splits] x 2
+  float *ws_o, *ws_m, *ws_l;  // partials: [parts, D], [parts] x 2; parts as the kernel lays them out
   int64_t n_tok;
   int B, Hq, Hkv, G, T, max_blocks, shift, num_blocks;
-  int splits, chunk;        // the token axis: splits chunks of `chunk` tokens
+  int splits, chunk;        // q8_prefill: the token axis as splits chunks of `chunk` tokens
   float mult;               // scale * log2 e
   unsigned int* status;
 };
@@ -62,6 +62,12 @@ struct Q8Tiles {
   bool one, skip_long;
   int skip_short;
 };
+
+// q8_decode.cu: tiles of up to 8 nrg query rows, one share of the key tiles a warp; any dtype.  The workspace holds two
+// partials of 8 nrg rows for each worker.
+constexpr int kQ8DecodeWarps = 8;
+axr_status q8_decode_launch(axr_dtype dtype, int d, bool i8, int nrg, int grid, const Q8Attend& a, const Q8Tiles& tl,
+                            cudaStream_t st, const char* w);
 
 // q8_prefill.cu: tiles of up to 256 query rows on the tcgen05 tensor cores, queries and outputs fp16 (half) or bf16.
 constexpr int kQ8PrefillRows = 256;

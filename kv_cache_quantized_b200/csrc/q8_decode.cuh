@@ -1,18 +1,50 @@
-// Decode attention over the paged 8-bit cache: every warp is a worker over (row tile, KV head, split) items, a row
-// tile being up to 8 NRG query rows (tokens x heads of the group) of one sequence.
+// Decode attention over the paged 8-bit cache: every warp is a worker on an equal share of the batch's key tiles.
+//
+// The work is a flat sequence of 32-token key tiles: sequence after sequence, for each of its row tiles (up to 8 NRG
+// query rows: tokens x heads of the group) and KV heads, the tiles of that sequence's length.  Worker w takes tiles
+// [w S, (w + 1) S), S = ceil(total / workers) but at least kDecMinTiles, whatever units (row tile x KV head) they fall
+// into: lengths in the batch need not be alike, and nothing of the split depends on what the host knows.  A unit that
+// lies inside one share is finished there; a unit cut by a share's edge leaves a partial (m, l, o) in the share's slot
+// 0 (the unit the share begins in) or 1 (a later one), merged by q8_merge_kernel.
+//
+// A worker streams its tiles through a ring of its own: TMA boxes of 16 or 32 token rows (a pool block may end inside
+// a tile only at bt = 16), swizzled, each completing on the stage's mbarrier.  Block-table entries and scales of 32
+// tiles sit in the lanes' registers, fetched half a batch ahead.
 //
 // Both products run as mma.sync.m16n8k16 on fp16 operands: the codes enter exactly, the fp32 query and the softmax
 // weights as hi and lo fp16 planes that occupy rows 0..7 and 8..15 of the same A tile, so one MMA forms both partial
 // sums and carries about 22 bits of each factor.  Coordinates and tokens may be summed in any order, so each lane
-// reads 16-byte runs of a code row: of the key row 8 n + g the bytes [D/4 t, D/4 t + D/4), whose word s feeds k-step
-// s; of the value rows 2 t, 2 t + 1, 2 t + 8, 2 t + 9 the bytes [D/8 g, D/8 g + D/8), byte j going to n-tile j.  No
-// code passes through shared memory or a shuffle twice.
+// reads 16-byte runs of a code row: of the key rows 8 n + g the bytes [D/4 t, D/4 t + D/4), whose word s feeds k-step
+// s; of the value rows 2 t, 2 t + 1, 2 t + 8, 2 t + 9 (+ 16) the bytes [D/8 g, D/8 g + D/8), byte j going to n-tile j.
+// Every code is read from shared memory once, by 128-bit loads that the swizzle keeps free of bank conflicts.
+// (tcgen05 would need the codes as fp16 in shared memory, four times this traffic, for 4 to 16 query rows of 128.)
 #pragma once
 
-#include "q8_merge.cuh"
-#include "warp_mma.cuh"
+#include <cuda.h>
+
+#include "dense_stream.cuh"
+#include "q8_attend.cuh"
 
 namespace axr {
+
+constexpr int kDecTile = 32;      // tokens per tile
+constexpr int kDecMinTiles = 4;   // smallest share
+
+template <int D>
+struct DecodePlan {
+  static constexpr int WARPS = kQ8DecodeWarps;
+  static constexpr int NS = 3;                              // stages per warp
+  static constexpr size_t PLANE = kDecTile * D;             // the K (or V) codes of a stage
+  static constexpr size_t STAGE = 2 * PLANE;
+  static constexpr size_t OFF_MBAR = WARPS * NS * STAGE;
+  static constexpr size_t bytes = 1024 + OFF_MBAR + WARPS * NS * 8;
+};
+
+__device__ __forceinline__ float q8_ex2(float x) {  // relative error 2^-22, as the planes'
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
 
 // 8-bit codes of two rows, 4 coordinates each, as 4 half2 (row a's coordinate, row b's coordinate)
 template <bool I8>
@@ -21,29 +53,152 @@ __device__ __forceinline__ void q8_pairs(uint32_t a, uint32_t b, uint32_t (&h)[4
   q8_halves<I8>(__byte_perm(a, b, 0x7362), h[2], h[3]);
 }
 
+// Byte offset in a plane of the 16-byte chunk c of row r: the TMA swizzles of 128-byte and 64-byte rows.
+template <int D>
+__device__ __forceinline__ uint32_t q8_swz(int r, int c) {
+  if constexpr (D == 128) return static_cast<uint32_t>(r * 128 + ((c ^ (r & 7)) << 4));
+  else return static_cast<uint32_t>(r * 64 + ((c ^ ((r >> 1) & 3)) << 4));
+}
+
+// Row tiles and key tiles of a sequence.
+struct Q8Extent {
+  int rts;    // row tiles
+  int tiles;  // key tiles of each (those of its last row tile)
+};
+__device__ __forceinline__ Q8Extent q8_extent(const Q8Attend& a, const Q8Tiles& tl, int b) {
+  const Q8Span sp = q8_span(a, b);
+  Q8Extent e;
+  e.rts = tl.one && sp.count > tl.tpt ? 0 : (sp.count + tl.tpt - 1) / tl.tpt;
+  e.tiles = e.rts > 0 ? (sp.len + kDecTile - 1) / kDecTile : 0;
+  return e;
+}
+
+// The flat tile sequence: where sequence b's tiles begin (begin), and how many there are in all (total).  One warp.
+// find >= 0: b is instead the sequence that holds flat tile `find`.
+__device__ __forceinline__ void q8_flat(const Q8Attend& a, const Q8Tiles& tl, int lane, int64_t find, int& b,
+                                        int64_t& begin, int64_t& total) {
+  int64_t sum = 0, at = 0;
+  int hit = b;
+  for (int b0 = 0; b0 < a.B; b0 += 32) {
+    int64_t n = 0;
+    if (b0 + lane < a.B) {
+      const Q8Extent e = q8_extent(a, tl, b0 + lane);
+      n = static_cast<int64_t>(e.rts) * a.Hkv * e.tiles;
+    }
+    int64_t inc = n;
+#pragma unroll
+    for (int m = 1; m < 32; m <<= 1) {
+      const int64_t o = __shfl_up_sync(0xffffffffu, inc, m);
+      if (lane >= m) inc += o;
+    }
+    const int64_t ex = sum + inc - n;  // tiles before this lane's sequence
+    const bool mine = find >= 0 ? n > 0 && ex <= find && find < ex + n : b0 + lane == b;
+    const unsigned who = __ballot_sync(0xffffffffu, mine);
+    if (who) {
+      hit = b0 + __ffs(who) - 1;
+      at = __shfl_sync(0xffffffffu, ex, __ffs(who) - 1);
+    }
+    sum += __shfl_sync(0xffffffffu, inc, 31);
+  }
+  b = hit;
+  begin = at;
+  total = sum;
+}
+
+__device__ __forceinline__ int64_t q8_share(int64_t total, int workers) {
+  const int64_t s = (total + workers - 1) / workers;
+  return s > kDecMinTiles ? s : kDecMinTiles;
+}
+
 template <typename T, int D, bool I8, int NRG>
-__global__ void __launch_bounds__(128) q8_decode_kernel(const __grid_constant__ Q8Attend a, const Q8Tiles tl) {
+__global__ void __launch_bounds__(32 * kQ8DecodeWarps, 1)
+q8_decode_kernel(const __grid_constant__ Q8Attend a, const __grid_constant__ Q8Tiles tl,
+                 const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap) {
+  using P = DecodePlan<D>;
   constexpr int KS = D / 16;       // k-steps of the score MMA, and 32-bit words of a lane's key run
   constexpr int NO = D / 8;        // n-tiles of the output
   constexpr int VB = D / 8;        // bytes of a lane's value run
   constexpr int ROWS = 8 * NRG;
-  const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  const int64_t worker = static_cast<int64_t>(blockIdx.x) * (blockDim.x >> 5) + (threadIdx.x >> 5);
-  const int64_t workers = static_cast<int64_t>(gridDim.x) * (blockDim.x >> 5);
-  const int64_t items = tl.tiles * a.Hkv * a.splits;
+  constexpr int NS = P::NS;
+  extern __shared__ __align__(16) uint8_t smem_raw[];
+  uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
+  uint8_t* ring = smem + static_cast<size_t>(warp) * NS * P::STAGE;
+  uint64_t* mbar = reinterpret_cast<uint64_t*>(smem + P::OFF_MBAR) + warp * NS;
+  if (lane == 0)
+    for (int s = 0; s < NS; ++s) tc::mbar_init(mbar + s, 1);
+  __syncwarp();
 
-  for (int64_t item = worker; item < items; item += workers) {
-    const int split = static_cast<int>(item % a.splits);
-    const int hk = static_cast<int>((item / a.splits) % a.Hkv);
-    const int64_t tile = item / (static_cast<int64_t>(a.splits) * a.Hkv);
-    int b;
-    int64_t i0;                    // first query token of the tile, in its sequence
-    q8_tile(a, tl, tile, lane, b, i0);
+  // shares are dealt across the blocks first, so that few of them still spread over every SM
+  const int workers = gridDim.x * P::WARPS;
+  const int worker = blockIdx.x + gridDim.x * warp;
+  int b = 0;
+  int64_t seq0 = 0, total = 0;
+  q8_flat(a, tl, lane, 0, b, seq0, total);
+  const int64_t S = q8_share(total, workers);
+  const int64_t x0 = worker * S, x1 = min(x0 + S, total);
+  const bool wide = a.shift >= 5;  // a 32-token tile lies in one pool block
+  uint32_t seq = 0;                // tiles consumed: stage seq % NS, phase parity (seq / NS) & 1
+  bool failed = false;
+
+  for (int64_t x = x0; x < x1;) {
+    q8_flat(a, tl, lane, x, b, seq0, total);
+    const Q8Extent ext = q8_extent(a, tl, b);
     const Q8Span sp = q8_span(a, b);
-    if (!q8_tile_live(a, tl, sp, i0, lane)) continue;
-    const int nrow = min(tl.tpt, sp.count - static_cast<int>(i0)) * a.G;
-    const int t_end = sp.pos0 + static_cast<int>(i0) + nrow / a.G;      // keys the tile's last token sees
-    const int begin = split * a.chunk, end = min(begin + a.chunk, t_end);
+    const int u = static_cast<int>((x - seq0) / ext.tiles);       // unit in the sequence: row tile, then KV head
+    const int k0 = static_cast<int>((x - seq0) % ext.tiles);      // first key tile
+    const int k1 = static_cast<int>(min(static_cast<int64_t>(ext.tiles), k0 + (x1 - x)));
+    const int hk = u % a.Hkv, i0 = u / a.Hkv * tl.tpt;
+    const int slot = x == x0 ? 0 : 1;
+    const bool whole = k0 == 0 && k1 == ext.tiles;
+    x += k1 - k0;
+    const int nrow = min(tl.tpt, sp.count - i0) * a.G;
+    const int t_end = sp.pos0 + i0 + nrow / a.G;                  // keys the row tile's last token sees
+    const int end = min(k1 * kDecTile, t_end);
+    const int ntiles = failed ? 0 : max(0, (end + kDecTile - 1) / kDecTile - k0);
+
+    // lane l: the pool's scale blocks (16 rows each) of key tile k0 + 32 i + l, -1 past the end, and their scales
+    auto blocks_of = [&](int i, int& r0, int& r1) {
+      const int t0 = (k0 + 32 * i + lane) * kDecTile;
+      r0 = r1 = -1;
+      if (t0 < end) r0 = static_cast<int>(q8_row(a, b, hk, t0) >> 4);
+      if (t0 + 16 < end) r1 = wide ? r0 + 1 : static_cast<int>(q8_row(a, b, hk, t0 + 16) >> 4);
+    };
+    auto scales_of = [&](int r0, int r1, float (&sc)[4]) {
+      sc[0] = r0 >= 0 ? __ldg(a.kscales + r0) : 0.f;
+      sc[1] = r1 >= 0 ? __ldg(a.kscales + r1) : 0.f;
+      sc[2] = r0 >= 0 ? __ldg(a.vscales + r0) : 0.f;
+      sc[3] = r1 >= 0 ? __ldg(a.vscales + r1) : 0.f;
+    };
+    int r0, r1, n0 = -1, n1 = -1;
+    float sc[4], scn[4] = {0.f, 0.f, 0.f, 0.f};
+    blocks_of(0, r0, r1);
+
+    // tile i of the unit into stage (seq + i) % NS; rows past the end are other rows of the pool, masked below
+    auto issue = [&](int i) {
+      const int from = i & 31;
+      const bool later = (i >> 5) != 0;  // relative to the batch the registers hold
+      const int y0 = __shfl_sync(0xffffffffu, later ? n0 : r0, from), y1 = __shfl_sync(0xffffffffu, later ? n1 : r1, from);
+      if (lane == 0) {
+        const int s = static_cast<int>(seq % NS);
+        uint8_t* st = ring + static_cast<size_t>(s) * P::STAGE;
+        const bool two = !wide && y1 >= 0;
+        mbar_arrive_expect_tx(mbar + s, static_cast<uint32_t>(2 * D * (wide ? 32 : two ? 32 : 16)));
+        tma_load_2d(st, &kmap, 0, y0 * 16, mbar + s);
+        tma_load_2d(st + P::PLANE, &vmap, 0, y0 * 16, mbar + s);
+        if (two) {
+          tma_load_2d(st + 16 * D, &kmap, 0, y1 * 16, mbar + s);
+          tma_load_2d(st + P::PLANE + 16 * D, &vmap, 0, y1 * 16, mbar + s);
+        }
+      }
+    };
+    const uint32_t seq_unit = seq;
+    for (int i = 0; i < NS && i < ntiles; ++i) {
+      issue(i);
+      ++seq;  // while issuing, seq names the stage
+    }
+    seq = seq_unit;
+    scales_of(r0, r1, sc);
 
     // the rows of this lane: row 8 n + g of group n, its last visible key, and its query operand
     uint32_t qf[NRG][KS][4];
@@ -55,18 +210,25 @@ __global__ void __launch_bounds__(128) q8_decode_kernel(const __grid_constant__ 
     for (int n = 0; n < NRG; ++n) {
       const int r = 8 * n + g;
       live[n] = r < nrow;
-      const int i = static_cast<int>(i0) + (live[n] ? r / a.G : 0), h = hk * a.G + (live[n] ? r % a.G : 0);
+      const int i = i0 + (live[n] ? r / a.G : 0), h = hk * a.G + (live[n] ? r % a.G : 0);
       lim[n] = live[n] ? min(sp.pos0 + i + 1, end) : 0;
       orow[n] = (sp.first + i) * a.Hq + h;
-      const T* src = static_cast<const T*>(a.q) + (sp.first + i) * a.q_stride + static_cast<int64_t>(h) * D + (D / 4) * t;
-      float x[KS][4], mx = 0.f;
+      const T* src =
+          static_cast<const T*>(a.q) + (sp.first + i) * a.q_stride + static_cast<int64_t>(h) * D + (D / 4) * t;
+      float v[KS][4], mx = 0.f;
 #pragma unroll
-      for (int s = 0; s < KS; ++s)
+      for (int s = 0; s < KS; s += 2) {
+        Raw8<T> w;
+        float y[8];
+        if (live[n]) w.load(src + 4 * s);
+        else w.zero();
+        w.values(y);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          x[s][e] = live[n] ? to_float<T>(src[4 * s + e]) : 0.f;
-          mx = fmaxf(mx, fabsf(x[s][e]));
+        for (int e = 0; e < 8; ++e) {
+          v[s + (e >> 2)][e & 3] = y[e];
+          mx = fmaxf(mx, fabsf(y[e]));
         }
+      }
       mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
       mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
       // a power of two that brings the row's largest magnitude to [2^13, 2^14): both planes keep their precision
@@ -77,8 +239,8 @@ __global__ void __launch_bounds__(128) q8_decode_kernel(const __grid_constant__ 
       f_row[n] = a.mult * ldexpf(1.f, ex);
 #pragma unroll
       for (int s = 0; s < KS; ++s) {
-        split_h2(x[s][0] * up, x[s][1] * up, qf[n][s][0], qf[n][s][1]);
-        split_h2(x[s][2] * up, x[s][3] * up, qf[n][s][2], qf[n][s][3]);
+        split_h2(v[s][0] * up, v[s][1] * up, qf[n][s][0], qf[n][s][1]);
+        split_h2(v[s][2] * up, v[s][3] * up, qf[n][s][2], qf[n][s][3]);
       }
     }
 
@@ -95,49 +257,57 @@ __global__ void __launch_bounds__(128) q8_decode_kernel(const __grid_constant__ 
         for (int e = 0; e < 4; ++e) o[n][j][e] = 0.f;
     }
 
-    for (int t0 = begin; t0 < end; t0 += kQ8Block) {
-      const int64_t row = q8_row(a, b, hk, t0);
-      const float ks = a.kscales[row >> 4], vs = a.vscales[row >> 4];
-      const uint8_t* kp = a.kcodes + row * D;
-      const uint8_t* vp = a.vcodes + row * D;
-      uint32_t kw[2][KS], vw[4][VB / 4];
+    for (int i = 0; i < ntiles; ++i) {
+      const int bi = i & 31;
+      if (bi == 0 && i > 0) {      // the next batch of 32 tiles moves in
+        r0 = n0; r1 = n1;
 #pragma unroll
-      for (int n = 0; n < 2; ++n)
-#pragma unroll
-        for (int s = 0; s < KS; s += 4)
-          *reinterpret_cast<uint4*>(&kw[n][s]) = *reinterpret_cast<const uint4*>(kp + (8 * n + g) * D + (D / 4) * t + 4 * s);
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const int tok = 2 * t + (r & 1) + 8 * (r >> 1);
-        if constexpr (VB == 16) *reinterpret_cast<uint4*>(vw[r]) = *reinterpret_cast<const uint4*>(vp + tok * D + VB * g);
-        else *reinterpret_cast<uint2*>(vw[r]) = *reinterpret_cast<const uint2*>(vp + tok * D + VB * g);
-        if (t0 + tok >= end) {  // rows no query sees may hold anything (an e4m3 NaN): their weight is zero, so are they
-#pragma unroll
-          for (int s = 0; s < VB / 4; ++s) vw[r][s] = 0u;
-        }
+        for (int e = 0; e < 4; ++e) sc[e] = scn[e];
       }
+      if (bi == 8 && i + 24 < ntiles) blocks_of((i >> 5) + 1, n0, n1);
+      if (bi == 16 && i + 16 < ntiles) scales_of(n0, n1, scn);
+      const float ks[2] = {__shfl_sync(0xffffffffu, sc[0], bi), __shfl_sync(0xffffffffu, sc[1], bi)};
+      const float vs[2] = {__shfl_sync(0xffffffffu, sc[2], bi), __shfl_sync(0xffffffffu, sc[3], bi)};
+      const int s = static_cast<int>(seq % NS);
+      if (!__all_sync(0xffffffffu, tc::mbar_wait(mbar + s, (seq / NS) & 1))) {
+        // a wait gave up: let this warp's copies in flight land, bounded again, before the block may exit
+        failed = true;
+        for (int j = 0; j < NS && i + j < ntiles; ++j) tc::mbar_wait(mbar + (seq + j) % NS, ((seq + j) / NS) & 1);
+        break;
+      }
+      const uint8_t* sK = ring + static_cast<size_t>(s) * P::STAGE;
+      const uint8_t* sV = sK + P::PLANE;
+      const int t0 = (k0 + i) * kDecTile;
+      const bool tail = t0 + kDecTile > sp.pos0 + i0 + 1 || t0 + kDecTile > end;  // some key is hidden from some row
 
-      // S = Q K^T for 16 tokens; lane (g, t) holds tokens 8 n' + 2 t + {0, 1} of row g
-      float sc[NRG][2][4];
+      // S = Q K^T for 32 tokens; lane (g, t) holds tokens 8 k + 2 t + {0, 1} of row g
+      float sc4[NRG][4][4];
 #pragma unroll
       for (int n = 0; n < NRG; ++n)
 #pragma unroll
-        for (int k = 0; k < 2; ++k)
+        for (int k = 0; k < 4; ++k)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) sc[n][k][e] = 0.f;
+          for (int e = 0; e < 4; ++e) sc4[n][k][e] = 0.f;
 #pragma unroll
-      for (int s = 0; s < KS; ++s)
+      for (int c = 0; c < KS / 4; ++c)
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          uint32_t b0, b1;
-          q8_halves<I8>(kw[k][s], b0, b1);
+        for (int k = 0; k < 4; ++k) {
+          const uint4 w4 = *reinterpret_cast<const uint4*>(sK + q8_swz<D>(8 * k + g, (KS / 4) * t + c));
+          const uint32_t w[4] = {w4.x, w4.y, w4.z, w4.w};
 #pragma unroll
-          for (int n = 0; n < NRG; ++n)
-            mma16816(sc[n][k], qf[n][s][0], qf[n][s][1], qf[n][s][2], qf[n][s][3], b0, b1);
+          for (int e = 0; e < 4; ++e) {
+            uint32_t b0, b1;
+            q8_halves<I8>(w[e], b0, b1);
+#pragma unroll
+            for (int n = 0; n < NRG; ++n)
+              mma16816(sc4[n][k], qf[n][4 * c + e][0], qf[n][4 * c + e][1], qf[n][4 * c + e][2], qf[n][4 * c + e][3],
+                       b0, b1);
+          }
         }
 
-      if (vs > vref) {  // uniform
-        const float up = __uint_as_float((__float_as_uint(vs) + 0x7fffffu) & 0x7f800000u);
+      const float vmax = fmaxf(vs[0], vs[1]);
+      if (vmax > vref) {  // uniform
+        const float up = __uint_as_float((__float_as_uint(vmax) + 0x7fffffu) & 0x7f800000u);
         const float f = vref / up;
         vref = up;
 #pragma unroll
@@ -147,32 +317,34 @@ __global__ void __launch_bounds__(128) q8_decode_kernel(const __grid_constant__ 
 #pragma unroll
             for (int e = 0; e < 4; ++e) o[n][j][e] *= f;
       }
-      const float vf = vref > 0.f ? vs / vref * 16384.f : 0.f;
+      // weights are formed relative to vref and 2^14 up: at most 2^14 in fp16, the lo plane's last step 2^-24
+      const float vi = vref > 0.f ? 16384.f / vref : 0.f;
+      const float vf[2] = {vs[0] * vi, vs[1] * vi};
 
-      uint32_t pf[NRG][4];
+      uint32_t pf[NRG][2][4];
 #pragma unroll
       for (int n = 0; n < NRG; ++n) {
-        float p[4], mx = -INFINITY;
-        const float f = f_row[n] * ks;
+        float p[8], mx = -INFINITY;
+        const float f[2] = {f_row[n] * ks[0], f_row[n] * ks[1]};
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int tok = t0 + 8 * (e >> 1) + 2 * t + (e & 1);
-          const float v = (sc[n][e >> 1][e & 1] + sc[n][e >> 1][2 + (e & 1)]) * f;
-          p[e] = tok < lim[n] ? v : -INFINITY;
+        for (int e = 0; e < 8; ++e) {
+          const int k = e >> 1;
+          const float v = (sc4[n][k][e & 1] + sc4[n][k][2 + (e & 1)]) * f[k >> 1];
+          p[e] = !tail || t0 + 8 * k + 2 * t + (e & 1) < lim[n] ? v : -INFINITY;
           mx = fmaxf(mx, p[e]);
         }
         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
         const float m_new = fmaxf(m_run[n], mx);
         const float m_use = m_new == -INFINITY ? 0.f : m_new;
-        const float alpha = exp2f(m_run[n] - m_use);
+        const float alpha = q8_ex2(m_run[n] - m_use);
         m_run[n] = m_new;
         float ps = 0.f;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          p[e] = exp2f(p[e] - m_use);
+        for (int e = 0; e < 8; ++e) {
+          p[e] = q8_ex2(p[e] - m_use);
           ps += p[e];
-          p[e] *= vf;
+          p[e] *= vf[e >> 2];
         }
         l_part[n] = l_part[n] * alpha + ps;
         if (__any_sync(0xffffffffu, alpha != 1.f)) {
@@ -181,26 +353,58 @@ __global__ void __launch_bounds__(128) q8_decode_kernel(const __grid_constant__ 
 #pragma unroll
             for (int e = 0; e < 4; ++e) o[n][j][e] *= alpha;  // rows g and g + 8 are planes of one row
         }
-        split_h2(p[0], p[1], pf[n][0], pf[n][1]);
-        split_h2(p[2], p[3], pf[n][2], pf[n][3]);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          split_h2(p[4 * h], p[4 * h + 1], pf[n][h][0], pf[n][h][1]);
+          split_h2(p[4 * h + 2], p[4 * h + 3], pf[n][h][2], pf[n][h][3]);
+        }
       }
 
       // O += P V
 #pragma unroll
-      for (int s = 0; s < VB / 4; ++s) {
-        uint32_t b0[4], b1[4];
-        q8_pairs<I8>(vw[0][s], vw[1][s], b0);
-        q8_pairs<I8>(vw[2][s], vw[3][s], b1);
+      for (int h = 0; h < 2; ++h) {
+        uint32_t vw[4][VB / 4];
 #pragma unroll
-        for (int n = 0; n < NRG; ++n)
+        for (int r = 0; r < 4; ++r) {
+          const int row = 16 * h + 2 * t + (r & 1) + 8 * (r >> 1);
+          if constexpr (VB == 16) {
+            *reinterpret_cast<uint4*>(vw[r]) = *reinterpret_cast<const uint4*>(sV + q8_swz<D>(row, g));
+          } else {
+            *reinterpret_cast<uint2*>(vw[r]) =
+                *reinterpret_cast<const uint2*>(sV + q8_swz<D>(row, g >> 1) + 8 * (g & 1));
+          }
+          if (tail && t0 + row >= end) {  // rows no query sees may hold anything (an e4m3 NaN): their weight is zero,
 #pragma unroll
-          for (int e = 0; e < 4; ++e)
-            mma16816(o[n][4 * s + e], pf[n][0], pf[n][1], pf[n][2], pf[n][3], b0[e], b1[e]);
+            for (int e = 0; e < VB / 4; ++e) vw[r][e] = 0u;  // so are they
+          }
+        }
+#pragma unroll
+        for (int e = 0; e < VB / 4; ++e) {
+          uint32_t b0[4], b1[4];
+          q8_pairs<I8>(vw[0][e], vw[1][e], b0);
+          q8_pairs<I8>(vw[2][e], vw[3][e], b1);
+#pragma unroll
+          for (int n = 0; n < NRG; ++n)
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              mma16816(o[n][4 * e + j], pf[n][h][0], pf[n][h][1], pf[n][h][2], pf[n][h][3], b0[j], b1[j]);
+        }
       }
+
+      // the stage is free once every lane's reads of it are done
+      fence_proxy_async();
+      __syncwarp();
+      if (i + NS < ntiles) issue(bi + NS);
+      ++seq;
+    }
+    if (failed) {
+      // what this warp owns from here on, this unit and the rest of its share, goes out as NaN
+#pragma unroll
+      for (int n = 0; n < NRG; ++n) m_run[n] = l_part[n] = __int_as_float(0x7fc00000);
     }
 
-    // the rows' partials, or their outputs when the axis is not split; lane (g, t) holds coordinates
-    // D/4 t + j (e = 0) and D/4 t + D/8 + j (e = 1)
+    // the rows' outputs, or their partials when the unit is cut; lane (g, t) holds coordinates D/4 t + j (e = 0) and
+    // D/4 t + D/8 + j (e = 1)
     const float unscale = vref * (1.f / 16384.f);
 #pragma unroll
     for (int n = 0; n < NRG; ++n) {
@@ -208,31 +412,86 @@ __global__ void __launch_bounds__(128) q8_decode_kernel(const __grid_constant__ 
       l += __shfl_xor_sync(0xffffffffu, l, 1);
       l += __shfl_xor_sync(0xffffffffu, l, 2);
       if (!live[n]) continue;
-      if (a.splits == 1) {
-        const float f = l > 0.f ? unscale / l : 0.f;
+      if (whole) {
+        const float f = l > 0.f ? unscale / l : l == 0.f ? 0.f : l;  // NaN stays
         T* dst = static_cast<T*>(a.out) + orow[n] * D + (D / 4) * t;
 #pragma unroll
         for (int e = 0; e < 2; ++e)
 #pragma unroll
-          for (int j = 0; j < NO; ++j)
-            dst[(D / 8) * e + j] = from_float<T>(l > 0.f ? (o[n][j][e] + o[n][j][2 + e]) * f : 0.f);
+          for (int j = 0; j < NO; j += 8) {
+            float y[8];
+#pragma unroll
+            for (int z = 0; z < 8; ++z) y[z] = l == 0.f ? 0.f : (o[n][j + z][e] + o[n][j + z][2 + e]) * f;
+            store8(dst + (D / 8) * e + j, y);
+          }
       } else {
-        const int64_t part = ((tile * a.Hkv + hk) * ROWS + 8 * n + g) * a.splits + split;
+        const int64_t part = (static_cast<int64_t>(worker) * 2 + slot) * ROWS + 8 * n + g;
         float* dst = a.ws_o + part * D + (D / 4) * t;
 #pragma unroll
         for (int e = 0; e < 2; ++e)
 #pragma unroll
-          for (int j = 0; j < NO; j += 4)
-            *reinterpret_cast<float4*>(dst + (D / 8) * e + j) =
-                make_float4((o[n][j][e] + o[n][j][2 + e]) * unscale, (o[n][j + 1][e] + o[n][j + 1][2 + e]) * unscale,
-                            (o[n][j + 2][e] + o[n][j + 2][2 + e]) * unscale,
-                            (o[n][j + 3][e] + o[n][j + 3][2 + e]) * unscale);
+          for (int j = 0; j < NO; j += 8) {
+            float y[8];
+#pragma unroll
+            for (int z = 0; z < 8; ++z) y[z] = (o[n][j + z][e] + o[n][j + z][2 + e]) * unscale;
+            store8(dst + (D / 8) * e + j, y);
+          }
         if (t == 0) {
           a.ws_m[part] = m_run[n];
           a.ws_l[part] = l;
         }
       }
     }
+  }
+  if (failed && lane == 0) atomicOr(a.status, 1u);
+}
+
+// Merge of the units cut by a share's edge, one block a unit, a warp a row: weights 2^(m_s - max m).  Units that a
+// worker finished are left alone; units of sequences without keys get zeros.  Launched as a programmatic dependent.
+template <typename T, int D>
+__global__ void __launch_bounds__(256)
+q8_decode_merge_kernel(const __grid_constant__ Q8Attend a, const __grid_constant__ Q8Tiles tl, int rows, int workers) {
+  constexpr int V = D / 32;
+  const int lane = threadIdx.x & 31, hk = static_cast<int>(blockIdx.x % a.Hkv);
+  int b;
+  int64_t i0;
+  q8_tile(a, tl, blockIdx.x / a.Hkv, lane, b, i0);
+  const Q8Span sp = q8_span(a, b);
+  if (!q8_tile_live(a, tl, sp, i0, threadIdx.x)) return;
+  int64_t seq0, total;
+  q8_flat(a, tl, lane, -1, b, seq0, total);
+  const int64_t S = q8_share(total, workers);
+  const Q8Extent ext = q8_extent(a, tl, b);
+  const int64_t p0 = seq0 + (i0 / tl.tpt * a.Hkv + hk) * ext.tiles, p1 = p0 + ext.tiles;  // the unit's flat tiles
+  const int nrow = min(tl.tpt, sp.count - static_cast<int>(i0)) * a.G;
+  const int w0 = static_cast<int>(p0 / S), w1 = static_cast<int>(p1 > p0 ? (p1 - 1) / S : w0);
+  asm volatile("griddepcontrol.wait;\n" ::: "memory");  // the partials are complete and visible after this
+  if (w0 == w1 && p1 > p0) return;                       // one worker finished it
+  for (int r = threadIdx.x >> 5; r < nrow; r += 8) {
+    float M = -INFINITY, L = 0.f, acc[V];
+#pragma unroll
+    for (int e = 0; e < V; ++e) acc[e] = 0.f;
+    if (p1 > p0) {
+      auto part = [&](int w) { return (static_cast<int64_t>(w) * 2 + (p0 <= w * S ? 0 : 1)) * rows + r; };
+      for (int w = w0 + lane; w <= w1; w += 32) M = fmaxf(M, a.ws_m[part(w)]);  // drops a NaN, which comes back in the sums
+      M = warp_max(M);
+#pragma unroll 4
+      for (int w = w0; w <= w1; ++w) {
+        const int64_t pt = part(w);
+        const float m = a.ws_m[pt], f = M == -INFINITY ? 0.f : q8_ex2(m - M);
+        const float* o = a.ws_o + pt * D + V * lane;
+        float y[V];
+#pragma unroll
+        for (int e = 0; e < V; ++e) y[e] = o[e];
+        L = fmaf(f, a.ws_l[pt], L);
+#pragma unroll
+        for (int e = 0; e < V; ++e) acc[e] = fmaf(f, y[e], acc[e]);
+      }
+    }
+    const int64_t orow = (sp.first + i0 + r / a.G) * a.Hq + static_cast<int64_t>(hk) * a.G + r % a.G;
+    T* dst = static_cast<T*>(a.out) + orow * D + V * lane;
+#pragma unroll
+    for (int e = 0; e < V; ++e) dst[e] = from_float<T>(L == 0.f ? 0.f : acc[e] / L);
   }
 }
 

@@ -1,4 +1,4 @@
-// Merge of the split partials of attention over the 8-bit cache.
+// Merge of q8_prefill_kernel's split partials.
 #pragma once
 
 #include "q8_attend.cuh"
