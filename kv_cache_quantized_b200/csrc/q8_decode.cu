@@ -19,6 +19,9 @@ axr_status launch(int grid, const Q8Attend& a, const Q8Tiles& tl, cudaStream_t s
   if ((rs = encode_byte_map(&kmap, a.kcodes, rows, D, box, w)) != AXR_OK) return rs;
   if ((rs = encode_byte_map(&vmap, a.vcodes, rows, D, box, w)) != AXR_OK) return rs;
   k<<<static_cast<unsigned>(grid), 32 * P::WARPS, P::bytes, st>>>(a, tl, kmap, vmap);
+  // the merge keeps the decode kernel's split of L1: another one would have to wait for every SM to drain
+  cudaFuncSetAttribute(q8_decode_merge_kernel<T, D>, cudaFuncAttributePreferredSharedMemoryCarveout,
+                       cudaSharedmemCarveoutMaxShared);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(tl.tiles * a.Hkv));
   cfg.blockDim = dim3(256);

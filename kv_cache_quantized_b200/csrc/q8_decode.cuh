@@ -11,12 +11,16 @@
 // a tile only at bt = 16), swizzled, each completing on the stage's mbarrier.  Block-table entries and scales of 32
 // tiles sit in the lanes' registers, fetched half a batch ahead.
 //
-// Both products run as mma.sync.m16n8k16 on fp16 operands: the codes enter exactly, the fp32 query and the softmax
-// weights as hi and lo fp16 planes that occupy rows 0..7 and 8..15 of the same A tile, so one MMA forms both partial
-// sums and carries about 22 bits of each factor.  Coordinates and tokens may be summed in any order, so each lane
-// reads 16-byte runs of a code row: of the key rows 8 n + g the bytes [D/4 t, D/4 t + D/4), whose word s feeds k-step
-// s; of the value rows 2 t, 2 t + 1, 2 t + 8, 2 t + 9 (+ 16) the bytes [D/8 g, D/8 g + D/8), byte j going to n-tile j.
-// Every code is read from shared memory once, by 128-bit loads that the swizzle keeps free of bank conflicts.
+// Both products run as mma.sync.m16n8k16 on fp16 operands with the query rows as the N side, so that no half of a tile
+// is empty for 8 rows:
+//   S^T = K Q^T    A = 16 tokens x 16 coordinates of codes, B = the queries;
+//   O^T += V^T P^T A = 16 coordinates x 16 tokens of codes, B = the weights, transposed in registers (movmatrix).
+// The codes enter exactly; queries and softmax weights as PL fp16 planes: hi and lo for fp32 (about 22 bits), one for
+// 16-bit queries and outputs (which a power of two makes exact; the weights round to 2^-11).  Coordinates and tokens may
+// be summed in any order, so each lane reads 16-byte runs of a code row: of the key rows 8 n + g the bytes
+// [D/4 t, D/4 t + D/4), whose word s feeds k-step s; of the value rows 2 t, 2 t + 1, 2 t + 8, 2 t + 9 (+ 16) the bytes
+// [D/8 g, D/8 g + D/8), bytes 2 j and 2 j + 1 going to rows g and g + 8 of coordinate tile j.  Every code is read from
+// shared memory once, by 128-bit loads that the swizzle keeps free of bank conflicts.
 // (tcgen05 would need the codes as fp16 in shared memory, four times this traffic, for 4 to 16 query rows of 128.)
 #pragma once
 
@@ -33,7 +37,7 @@ constexpr int kDecMinTiles = 4;   // smallest share
 template <int D>
 struct DecodePlan {
   static constexpr int WARPS = kQ8DecodeWarps;
-  static constexpr int NS = 3;                              // stages per warp
+  static constexpr int NS = 2;                              // stages per warp
   static constexpr size_t PLANE = kDecTile * D;             // the K (or V) codes of a stage
   static constexpr size_t STAGE = 2 * PLANE;
   static constexpr size_t OFF_MBAR = WARPS * NS * STAGE;
@@ -110,14 +114,22 @@ __device__ __forceinline__ int64_t q8_share(int64_t total, int workers) {
   return s > kDecMinTiles ? s : kDecMinTiles;
 }
 
+// The 8 x 8 matrix of 16-bit values held one row of pairs a lane group, transposed.
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+  uint32_t y;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+
 template <typename T, int D, bool I8, int NRG>
 __global__ void __launch_bounds__(32 * kQ8DecodeWarps, 1)
 q8_decode_kernel(const __grid_constant__ Q8Attend a, const __grid_constant__ Q8Tiles tl,
                  const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap) {
   using P = DecodePlan<D>;
+  constexpr int PL = sizeof(T) == 4 ? 2 : 1;  // fp16 planes of the queries and weights
   constexpr int KS = D / 16;       // k-steps of the score MMA, and 32-bit words of a lane's key run
-  constexpr int NO = D / 8;        // n-tiles of the output
-  constexpr int VB = D / 8;        // bytes of a lane's value run
+  constexpr int NO = D / 16;       // coordinate tiles of the output
+  constexpr int VB = D / 8;        // bytes of a lane's value run, and its output coordinates
   constexpr int ROWS = 8 * NRG;
   constexpr int NS = P::NS;
   extern __shared__ __align__(16) uint8_t smem_raw[];
@@ -200,19 +212,15 @@ q8_decode_kernel(const __grid_constant__ Q8Attend a, const __grid_constant__ Q8T
     seq = seq_unit;
     scales_of(r0, r1, sc);
 
-    // the rows of this lane: row 8 n + g of group n, its last visible key, and its query operand
-    uint32_t qf[NRG][KS][4];
-    float f_row[NRG];
-    int lim[NRG];                  // keys t < lim are visible
-    bool live[NRG];
-    int64_t orow[NRG];
+    // the query operand of this lane: row 8 n + g of group n, coordinates [D/4 t, D/4 t + D/4)
+    uint32_t qf[NRG][PL][KS][2];
+    float f_row[NRG][2];
+    int lim[NRG][2];               // rows 8 n + 2 t + {0, 1}, whose scores and output this lane holds: keys < lim are visible
 #pragma unroll
     for (int n = 0; n < NRG; ++n) {
       const int r = 8 * n + g;
-      live[n] = r < nrow;
-      const int i = i0 + (live[n] ? r / a.G : 0), h = hk * a.G + (live[n] ? r % a.G : 0);
-      lim[n] = live[n] ? min(sp.pos0 + i + 1, end) : 0;
-      orow[n] = (sp.first + i) * a.Hq + h;
+      const bool on = r < nrow;
+      const int i = i0 + (on ? r / a.G : 0), h = hk * a.G + (on ? r % a.G : 0);
       const T* src =
           static_cast<const T*>(a.q) + (sp.first + i) * a.q_stride + static_cast<int64_t>(h) * D + (D / 4) * t;
       float v[KS][4], mx = 0.f;
@@ -220,7 +228,7 @@ q8_decode_kernel(const __grid_constant__ Q8Attend a, const __grid_constant__ Q8T
       for (int s = 0; s < KS; s += 2) {
         Raw8<T> w;
         float y[8];
-        if (live[n]) w.load(src + 4 * s);
+        if (on) w.load(src + 4 * s);
         else w.zero();
         w.values(y);
 #pragma unroll
@@ -231,26 +239,33 @@ q8_decode_kernel(const __grid_constant__ Q8Attend a, const __grid_constant__ Q8T
       }
       mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
       mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-      // a power of two that brings the row's largest magnitude to [2^13, 2^14): both planes keep their precision
+      // a power of two that brings the row's largest magnitude to [2^13, 2^14): the planes keep their precision
       int ex = 0;
       if (mx > 0.f && isfinite(mx)) frexpf(mx, &ex);
       ex = max(-100, min(100, ex - 14));
-      const float up = ldexpf(1.f, -ex);
-      f_row[n] = a.mult * ldexpf(1.f, ex);
+      const float up = ldexpf(1.f, -ex), fr = a.mult * ldexpf(1.f, ex);
 #pragma unroll
-      for (int s = 0; s < KS; ++s) {
-        split_h2(v[s][0] * up, v[s][1] * up, qf[n][s][0], qf[n][s][1]);
-        split_h2(v[s][2] * up, v[s][3] * up, qf[n][s][2], qf[n][s][3]);
+      for (int s = 0; s < KS; ++s)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          if constexpr (PL == 2) split_h2(v[s][2 * e] * up, v[s][2 * e + 1] * up, qf[n][0][s][e], qf[n][1][s][e]);
+          else qf[n][0][s][e] = pack_h2(v[s][2 * e] * up, v[s][2 * e + 1] * up);
+        }
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int rr = 8 * n + 2 * t + e;
+        f_row[n][e] = __shfl_sync(0xffffffffu, fr, 4 * (2 * t + e));
+        lim[n][e] = rr < nrow ? min(sp.pos0 + i0 + rr / a.G + 1, end) : 0;
       }
     }
 
-    float o[NRG][NO][4];
-    float m_run[NRG], l_part[NRG];
+    float o[NRG][NO][4];           // coordinates VB g + 2 j + {0, 1} (registers 0 and 1, 2 and 3) of the two rows
+    float m_run[NRG][2], l_part[NRG][2];
     float vref = 0.f;              // power of two the weights' value scales are relative to
 #pragma unroll
     for (int n = 0; n < NRG; ++n) {
-      m_run[n] = -INFINITY;
-      l_part[n] = 0.f;
+      m_run[n][0] = m_run[n][1] = -INFINITY;
+      l_part[n][0] = l_part[n][1] = 0.f;
 #pragma unroll
       for (int j = 0; j < NO; ++j)
 #pragma unroll
@@ -280,28 +295,31 @@ q8_decode_kernel(const __grid_constant__ Q8Attend a, const __grid_constant__ Q8T
       const int t0 = (k0 + i) * kDecTile;
       const bool tail = t0 + kDecTile > sp.pos0 + i0 + 1 || t0 + kDecTile > end;  // some key is hidden from some row
 
-      // S = Q K^T for 32 tokens; lane (g, t) holds tokens 8 k + 2 t + {0, 1} of row g
-      float sc4[NRG][4][4];
+      // S^T = K Q^T for 32 tokens: registers 0, 1 are token 16 h + g of rows 2 t, 2 t + 1, registers 2, 3 token + 8
+      float sc4[NRG][2][4];
 #pragma unroll
       for (int n = 0; n < NRG; ++n)
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
+        for (int h = 0; h < 2; ++h)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) sc4[n][k][e] = 0.f;
+          for (int e = 0; e < 4; ++e) sc4[n][h][e] = 0.f;
 #pragma unroll
       for (int c = 0; c < KS / 4; ++c)
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const uint4 w4 = *reinterpret_cast<const uint4*>(sK + q8_swz<D>(8 * k + g, (KS / 4) * t + c));
-          const uint32_t w[4] = {w4.x, w4.y, w4.z, w4.w};
+        for (int h = 0; h < 2; ++h) {
+          const uint4 x4 = *reinterpret_cast<const uint4*>(sK + q8_swz<D>(16 * h + g, (KS / 4) * t + c));
+          const uint4 y4 = *reinterpret_cast<const uint4*>(sK + q8_swz<D>(16 * h + 8 + g, (KS / 4) * t + c));
+          const uint32_t wx[4] = {x4.x, x4.y, x4.z, x4.w}, wy[4] = {y4.x, y4.y, y4.z, y4.w};
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            uint32_t b0, b1;
-            q8_halves<I8>(w[e], b0, b1);
+            uint32_t a0, a1, a2, a3;
+            q8_halves<I8>(wx[e], a0, a2);
+            q8_halves<I8>(wy[e], a1, a3);
 #pragma unroll
             for (int n = 0; n < NRG; ++n)
-              mma16816(sc4[n][k], qf[n][4 * c + e][0], qf[n][4 * c + e][1], qf[n][4 * c + e][2], qf[n][4 * c + e][3],
-                       b0, b1);
+#pragma unroll
+              for (int p = 0; p < PL; ++p)
+                mma16816(sc4[n][h], a0, a1, a2, a3, qf[n][p][4 * c + e][0], qf[n][p][4 * c + e][1]);
           }
         }
 
@@ -321,46 +339,62 @@ q8_decode_kernel(const __grid_constant__ Q8Attend a, const __grid_constant__ Q8T
       const float vi = vref > 0.f ? 16384.f / vref : 0.f;
       const float vf[2] = {vs[0] * vi, vs[1] * vi};
 
-      uint32_t pf[NRG][2][4];
+      uint32_t pf[NRG][PL][2][2];
 #pragma unroll
       for (int n = 0; n < NRG; ++n) {
-        float p[8], mx = -INFINITY;
-        const float f[2] = {f_row[n] * ks[0], f_row[n] * ks[1]};
+        float p[2][4], mx[2] = {-INFINITY, -INFINITY}, m_use[2], alpha[2];  // [row][16 h + g, + 8]
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const int k = e >> 1;
-          const float v = (sc4[n][k][e & 1] + sc4[n][k][2 + (e & 1)]) * f[k >> 1];
-          p[e] = !tail || t0 + 8 * k + 2 * t + (e & 1) < lim[n] ? v : -INFINITY;
-          mx = fmaxf(mx, p[e]);
-        }
-        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-        const float m_new = fmaxf(m_run[n], mx);
-        const float m_use = m_new == -INFINITY ? 0.f : m_new;
-        const float alpha = q8_ex2(m_run[n] - m_use);
-        m_run[n] = m_new;
-        float ps = 0.f;
+        for (int r = 0; r < 2; ++r) {
+          const float f[2] = {f_row[n][r] * ks[0], f_row[n][r] * ks[1]};
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          p[e] = q8_ex2(p[e] - m_use);
-          ps += p[e];
-          p[e] *= vf[e >> 2];
+          for (int e = 0; e < 4; ++e) {
+            const int h = e >> 1;
+            const float v = sc4[n][h][2 * (e & 1) + r] * f[h];
+            p[r][e] = !tail || t0 + 16 * h + 8 * (e & 1) + g < lim[n][r] ? v : -INFINITY;
+            mx[r] = fmaxf(mx[r], p[r][e]);
+          }
         }
-        l_part[n] = l_part[n] * alpha + ps;
-        if (__any_sync(0xffffffffu, alpha != 1.f)) {
+#pragma unroll
+        for (int x = 4; x < 32; x <<= 1) {
+          mx[0] = fmaxf(mx[0], __shfl_xor_sync(0xffffffffu, mx[0], x));
+          mx[1] = fmaxf(mx[1], __shfl_xor_sync(0xffffffffu, mx[1], x));
+        }
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          const float m_new = fmaxf(m_run[n][r], mx[r]);
+          m_use[r] = m_new == -INFINITY ? 0.f : m_new;
+          alpha[r] = q8_ex2(m_run[n][r] - m_use[r]);
+          m_run[n][r] = m_new;
+          l_part[n][r] *= alpha[r];
+        }
+        if (__any_sync(0xffffffffu, alpha[0] != 1.f || alpha[1] != 1.f)) {
 #pragma unroll
           for (int j = 0; j < NO; ++j)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) o[n][j][e] *= alpha;  // rows g and g + 8 are planes of one row
+            for (int e = 0; e < 4; ++e) o[n][j][e] *= alpha[e & 1];
         }
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          split_h2(p[4 * h], p[4 * h + 1], pf[n][h][0], pf[n][h][1]);
-          split_h2(p[4 * h + 2], p[4 * h + 3], pf[n][h][2], pf[n][h][3]);
+        for (int r = 0; r < 2; ++r)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            p[r][e] = q8_ex2(p[r][e] - m_use[r]);
+            l_part[n][r] += p[r][e];
+            p[r][e] *= vf[e >> 1];
+          }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          if constexpr (PL == 2) {
+            uint32_t hi, lo;
+            split_h2(p[0][e], p[1][e], hi, lo);
+            pf[n][0][e >> 1][e & 1] = transpose8x8(hi);
+            pf[n][PL - 1][e >> 1][e & 1] = transpose8x8(lo);
+          } else {
+            pf[n][0][e >> 1][e & 1] = transpose8x8(pack_h2(p[0][e], p[1][e]));
+          }
         }
       }
 
-      // O += P V
+      // O^T += V^T P^T
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         uint32_t vw[4][VB / 4];
@@ -386,8 +420,11 @@ q8_decode_kernel(const __grid_constant__ Q8Attend a, const __grid_constant__ Q8T
 #pragma unroll
           for (int n = 0; n < NRG; ++n)
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-              mma16816(o[n][4 * e + j], pf[n][h][0], pf[n][h][1], pf[n][h][2], pf[n][h][3], b0[j], b1[j]);
+            for (int p = 0; p < PL; ++p)
+#pragma unroll
+              for (int j = 0; j < 2; ++j)
+                mma16816(o[n][2 * e + j], b0[2 * j], b0[2 * j + 1], b1[2 * j], b1[2 * j + 1], pf[n][p][h][0],
+                         pf[n][p][h][1]);
         }
       }
 
@@ -400,48 +437,45 @@ q8_decode_kernel(const __grid_constant__ Q8Attend a, const __grid_constant__ Q8T
     if (failed) {
       // what this warp owns from here on, this unit and the rest of its share, goes out as NaN
 #pragma unroll
-      for (int n = 0; n < NRG; ++n) m_run[n] = l_part[n] = __int_as_float(0x7fc00000);
+      for (int n = 0; n < NRG; ++n)
+#pragma unroll
+        for (int r = 0; r < 2; ++r) m_run[n][r] = l_part[n][r] = __int_as_float(0x7fc00000);
     }
 
-    // the rows' outputs, or their partials when the unit is cut; lane (g, t) holds coordinates D/4 t + j (e = 0) and
-    // D/4 t + D/8 + j (e = 1)
+    // the rows' outputs, or their partials when the unit is cut
     const float unscale = vref * (1.f / 16384.f);
 #pragma unroll
-    for (int n = 0; n < NRG; ++n) {
-      float l = l_part[n];
-      l += __shfl_xor_sync(0xffffffffu, l, 1);
-      l += __shfl_xor_sync(0xffffffffu, l, 2);
-      if (!live[n]) continue;
-      if (whole) {
-        const float f = l > 0.f ? unscale / l : l == 0.f ? 0.f : l;  // NaN stays
-        T* dst = static_cast<T*>(a.out) + orow[n] * D + (D / 4) * t;
+    for (int n = 0; n < NRG; ++n)
 #pragma unroll
-        for (int e = 0; e < 2; ++e)
+      for (int r = 0; r < 2; ++r) {
+        float l = l_part[n][r];
 #pragma unroll
-          for (int j = 0; j < NO; j += 8) {
-            float y[8];
+        for (int x = 4; x < 32; x <<= 1) l += __shfl_xor_sync(0xffffffffu, l, x);
+        const int row = 8 * n + 2 * t + r;
+        if (row >= nrow) continue;
+        const float f = !whole ? unscale : l == 0.f ? 0.f : unscale / l;  // NaN stays
+        float y[VB];
 #pragma unroll
-            for (int z = 0; z < 8; ++z) y[z] = l == 0.f ? 0.f : (o[n][j + z][e] + o[n][j + z][2 + e]) * f;
-            store8(dst + (D / 8) * e + j, y);
+        for (int j = 0; j < NO; ++j) {
+          y[2 * j] = whole && l == 0.f ? 0.f : o[n][j][r] * f;
+          y[2 * j + 1] = whole && l == 0.f ? 0.f : o[n][j][2 + r] * f;
+        }
+        if (whole) {
+          const int64_t orow = (sp.first + i0 + row / a.G) * a.Hq + static_cast<int64_t>(hk) * a.G + row % a.G;
+          T* dst = static_cast<T*>(a.out) + orow * D + VB * g;
+#pragma unroll
+          for (int j = 0; j < VB; j += 8) store8(dst + j, *reinterpret_cast<float(*)[8]>(y + j));
+        } else {
+          const int64_t part = (static_cast<int64_t>(worker) * 2 + slot) * ROWS + row;
+          float* dst = a.ws_o + part * D + VB * g;
+#pragma unroll
+          for (int j = 0; j < VB; j += 8) store8(dst + j, *reinterpret_cast<float(*)[8]>(y + j));
+          if (g == 0) {
+            a.ws_m[part] = m_run[n][r];
+            a.ws_l[part] = l;
           }
-      } else {
-        const int64_t part = (static_cast<int64_t>(worker) * 2 + slot) * ROWS + 8 * n + g;
-        float* dst = a.ws_o + part * D + (D / 4) * t;
-#pragma unroll
-        for (int e = 0; e < 2; ++e)
-#pragma unroll
-          for (int j = 0; j < NO; j += 8) {
-            float y[8];
-#pragma unroll
-            for (int z = 0; z < 8; ++z) y[z] = (o[n][j + z][e] + o[n][j + z][2 + e]) * unscale;
-            store8(dst + (D / 8) * e + j, y);
-          }
-        if (t == 0) {
-          a.ws_m[part] = m_run[n];
-          a.ws_l[part] = l;
         }
       }
-    }
   }
   if (failed && lane == 0) atomicOr(a.status, 1u);
 }
