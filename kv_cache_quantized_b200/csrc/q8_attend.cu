@@ -17,7 +17,7 @@ struct Q8Plan {
   size_t parts;   // partial rows in the workspace
 };
 
-// The warp-MMA kernel: one block per SM, fewer when shares of four key tiles would not fill them.
+// The warp-MMA kernel: one block per SM, fewer when shares of two key tiles would not fill them.
 Q8Plan plan_decode(int64_t n_tok, int B, int G, int Hkv, int T, bool one, int max_q) {
   Q8Plan pl;
   pl.nrg = (one ? static_cast<int64_t>(max_q) * G <= 8 : G <= 8 && n_tok <= B) ? 1 : 2;
@@ -28,7 +28,7 @@ Q8Plan plan_decode(int64_t n_tok, int B, int G, int Hkv, int T, bool one, int ma
   pl.tl.tiles = one ? B : n_tok / pl.tl.tpt + B;
   pl.sp.splits = 1;
   pl.sp.chunk = 0;
-  const int64_t shares = (pl.tl.tiles * Hkv * ((static_cast<int64_t>(T) + 31) / 32) + 3) / 4;
+  const int64_t shares = (pl.tl.tiles * Hkv * ((static_cast<int64_t>(T) + 31) / 32) + 1) / 2;
   pl.grid = static_cast<int>(shares < 1 ? 1 : shares < kSmCount ? shares : kSmCount);
   pl.parts = static_cast<size_t>(pl.grid) * kQ8DecodeWarps * 2 * 8 * pl.nrg;
   return pl;

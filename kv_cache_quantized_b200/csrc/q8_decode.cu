@@ -23,8 +23,8 @@ axr_status launch(int grid, const Q8Attend& a, const Q8Tiles& tl, cudaStream_t s
   cudaFuncSetAttribute(q8_decode_merge_kernel<T, D>, cudaFuncAttributePreferredSharedMemoryCarveout,
                        cudaSharedmemCarveoutMaxShared);
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(tl.tiles * a.Hkv));
-  cfg.blockDim = dim3(256);
+  cfg.gridDim = dim3(static_cast<unsigned>(tl.tiles * a.Hkv * tl.tpt * a.G));
+  cfg.blockDim = dim3(32 * kMergeWarps);
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

@@ -32,7 +32,7 @@
 namespace axr {
 
 constexpr int kDecTile = 32;      // tokens per tile
-constexpr int kDecMinTiles = 4;   // smallest share
+constexpr int kDecMinTiles = 2;   // smallest share
 
 template <int D>
 struct DecodePlan {
@@ -64,6 +64,12 @@ __device__ __forceinline__ uint32_t q8_swz(int r, int c) {
   else return static_cast<uint32_t>(r * 64 + ((c ^ ((r >> 1) & 3)) << 4));
 }
 
+// Quotient of non-negative values: 32-bit division where both fit (a 64-bit one takes about a hundred instructions).
+__device__ __forceinline__ int64_t q8_div(int64_t x, int64_t y) {
+  if (((x | y) >> 32) == 0) return static_cast<uint32_t>(x) / static_cast<uint32_t>(y);
+  return x / y;
+}
+
 // Row tiles and key tiles of a sequence.
 struct Q8Extent {
   int rts;    // row tiles
@@ -72,7 +78,7 @@ struct Q8Extent {
 __device__ __forceinline__ Q8Extent q8_extent(const Q8Attend& a, const Q8Tiles& tl, int b) {
   const Q8Span sp = q8_span(a, b);
   Q8Extent e;
-  e.rts = tl.one && sp.count > tl.tpt ? 0 : (sp.count + tl.tpt - 1) / tl.tpt;
+  e.rts = tl.one ? (sp.count > 0 && sp.count <= tl.tpt ? 1 : 0) : (sp.count + tl.tpt - 1) / tl.tpt;
   e.tiles = e.rts > 0 ? (sp.len + kDecTile - 1) / kDecTile : 0;
   return e;
 }
@@ -110,7 +116,7 @@ __device__ __forceinline__ void q8_flat(const Q8Attend& a, const Q8Tiles& tl, in
 }
 
 __device__ __forceinline__ int64_t q8_share(int64_t total, int workers) {
-  const int64_t s = (total + workers - 1) / workers;
+  const int64_t s = q8_div(total + workers - 1, workers);
   return s > kDecMinTiles ? s : kDecMinTiles;
 }
 
@@ -142,6 +148,7 @@ q8_decode_kernel(const __grid_constant__ Q8Attend a, const __grid_constant__ Q8T
   __syncwarp();
 
   // shares are dealt across the blocks first, so that few of them still spread over every SM
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the merge may get ready; it waits for this grid's end
   const int workers = gridDim.x * P::WARPS;
   const int worker = blockIdx.x + gridDim.x * warp;
   int b = 0;
@@ -157,8 +164,8 @@ q8_decode_kernel(const __grid_constant__ Q8Attend a, const __grid_constant__ Q8T
     q8_flat(a, tl, lane, x, b, seq0, total);
     const Q8Extent ext = q8_extent(a, tl, b);
     const Q8Span sp = q8_span(a, b);
-    const int u = static_cast<int>((x - seq0) / ext.tiles);       // unit in the sequence: row tile, then KV head
-    const int k0 = static_cast<int>((x - seq0) % ext.tiles);      // first key tile
+    const int u = static_cast<int>(q8_div(x - seq0, ext.tiles));  // unit in the sequence: row tile, then KV head
+    const int k0 = static_cast<int>(x - seq0 - static_cast<int64_t>(u) * ext.tiles);  // first key tile
     const int k1 = static_cast<int>(min(static_cast<int64_t>(ext.tiles), k0 + (x1 - x)));
     const int hk = u % a.Hkv, i0 = u / a.Hkv * tl.tpt;
     const int slot = x == x0 ? 0 : 1;
@@ -480,53 +487,98 @@ q8_decode_kernel(const __grid_constant__ Q8Attend a, const __grid_constant__ Q8T
   if (failed && lane == 0) atomicOr(a.status, 1u);
 }
 
-// Merge of the units cut by a share's edge, one block a unit, a warp a row: weights 2^(m_s - max m).  Units that a
-// worker finished are left alone; units of sequences without keys get zeros.  Launched as a programmatic dependent.
+// Merge of the units cut by a share's edge, one block a (unit, row): weights 2^(m_s - max m), the unit's partials dealt
+// over the block's warps, their sums added in warp order.  Rows that a worker finished are left alone; rows of sequences
+// without keys get zeros.  Launched as a programmatic dependent of the decode kernel.
+constexpr int kMergeWarps = 4;
 template <typename T, int D>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(32 * kMergeWarps)
 q8_decode_merge_kernel(const __grid_constant__ Q8Attend a, const __grid_constant__ Q8Tiles tl, int rows, int workers) {
   constexpr int V = D / 32;
-  const int lane = threadIdx.x & 31, hk = static_cast<int>(blockIdx.x % a.Hkv);
+  __shared__ float max_m[kMergeWarps], sum_l[kMergeWarps], sum_o[kMergeWarps][D];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int per = tl.tpt * a.G, r = static_cast<int>(blockIdx.x) % per, unit = static_cast<int>(blockIdx.x) / per;
+  const int hk = unit % a.Hkv;
   int b;
   int64_t i0;
-  q8_tile(a, tl, blockIdx.x / a.Hkv, lane, b, i0);
+  q8_tile(a, tl, unit / a.Hkv, lane, b, i0);
   const Q8Span sp = q8_span(a, b);
   if (!q8_tile_live(a, tl, sp, i0, threadIdx.x)) return;
+  if (r >= min(tl.tpt, sp.count - static_cast<int>(i0)) * a.G) return;
   int64_t seq0, total;
   q8_flat(a, tl, lane, -1, b, seq0, total);
   const int64_t S = q8_share(total, workers);
   const Q8Extent ext = q8_extent(a, tl, b);
-  const int64_t p0 = seq0 + (i0 / tl.tpt * a.Hkv + hk) * ext.tiles, p1 = p0 + ext.tiles;  // the unit's flat tiles
-  const int nrow = min(tl.tpt, sp.count - static_cast<int>(i0)) * a.G;
-  const int w0 = static_cast<int>(p0 / S), w1 = static_cast<int>(p1 > p0 ? (p1 - 1) / S : w0);
+  const int64_t p0 = seq0 + (q8_div(i0, tl.tpt) * a.Hkv + hk) * ext.tiles, p1 = p0 + ext.tiles;  // the unit's flat tiles
+  const int w0 = static_cast<int>(q8_div(p0, S)), n = p1 > p0 ? static_cast<int>(q8_div(p1 - 1, S)) - w0 + 1 : 0;
   asm volatile("griddepcontrol.wait;\n" ::: "memory");  // the partials are complete and visible after this
-  if (w0 == w1 && p1 > p0) return;                       // one worker finished it
-  for (int r = threadIdx.x >> 5; r < nrow; r += 8) {
-    float M = -INFINITY, L = 0.f, acc[V];
+  if (n == 1) return;                                     // one worker finished it
+  // partial k of the unit: slot 0 of worker w0 + k, but slot 1 of w0 where the unit begins inside its share
+  const int64_t first = (static_cast<int64_t>(w0) * 2 + (p0 > w0 * S ? 1 : 0)) * rows + r;
+  const int64_t rest = static_cast<int64_t>(w0) * 2 * rows + r;
+  auto part = [&](int k) { return k == 0 ? first : rest + static_cast<int64_t>(k) * 2 * rows; };
+  // each warp its partials, U at a time: all loads of a group are in flight before its maximum is known
+  constexpr int U = 8;
+  float M = -INFINITY, L = 0.f, acc[V];
 #pragma unroll
-    for (int e = 0; e < V; ++e) acc[e] = 0.f;
-    if (p1 > p0) {
-      auto part = [&](int w) { return (static_cast<int64_t>(w) * 2 + (p0 <= w * S ? 0 : 1)) * rows + r; };
-      for (int w = w0 + lane; w <= w1; w += 32) M = fmaxf(M, a.ws_m[part(w)]);  // drops a NaN, which comes back in the sums
-      M = warp_max(M);
-#pragma unroll 4
-      for (int w = w0; w <= w1; ++w) {
-        const int64_t pt = part(w);
-        const float m = a.ws_m[pt], f = M == -INFINITY ? 0.f : q8_ex2(m - M);
-        const float* o = a.ws_o + pt * D + V * lane;
-        float y[V];
+  for (int e = 0; e < V; ++e) acc[e] = 0.f;
+  for (int k0 = warp; k0 < n; k0 += U * kMergeWarps) {
+    float m[U], l[U], y[U][V];
 #pragma unroll
-        for (int e = 0; e < V; ++e) y[e] = o[e];
-        L = fmaf(f, a.ws_l[pt], L);
-#pragma unroll
-        for (int e = 0; e < V; ++e) acc[e] = fmaf(f, y[e], acc[e]);
+    for (int u = 0; u < U; ++u) {
+      const int k = k0 + u * kMergeWarps;
+      const bool on = k < n;
+      const int64_t pt = part(on ? k : k0);
+      m[u] = on ? __ldcg(a.ws_m + pt) : -INFINITY;
+      l[u] = on ? __ldcg(a.ws_l + pt) : 0.f;
+      const float* o = a.ws_o + pt * D + V * lane;
+      if constexpr (V == 4) {
+        const float4 q4 = __ldcg(reinterpret_cast<const float4*>(o));
+        y[u][0] = q4.x; y[u][1] = q4.y; y[u][2] = q4.z; y[u][3] = q4.w;
+      } else {
+        const float2 q2 = __ldcg(reinterpret_cast<const float2*>(o));
+        y[u][0] = q2.x; y[u][1] = q2.y;
       }
     }
-    const int64_t orow = (sp.first + i0 + r / a.G) * a.Hq + static_cast<int64_t>(hk) * a.G + r % a.G;
-    T* dst = static_cast<T*>(a.out) + orow * D + V * lane;
+    float top = M;
 #pragma unroll
-    for (int e = 0; e < V; ++e) dst[e] = from_float<T>(L == 0.f ? 0.f : acc[e] / L);
+    for (int u = 0; u < U; ++u) top = fmaxf(top, m[u]);   // drops a NaN, which comes back in the sums
+    const float back = top == -INFINITY ? 0.f : q8_ex2(M - top);
+    L *= back;
+#pragma unroll
+    for (int e = 0; e < V; ++e) acc[e] *= back;
+    M = top;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const bool on = k0 + u * kMergeWarps < n;
+      const float f = !on || M == -INFINITY ? 0.f : q8_ex2(m[u] - M);
+      L = fmaf(f, l[u], L);
+#pragma unroll
+      for (int e = 0; e < V; ++e) acc[e] = fmaf(f, y[u][e], acc[e]);
+    }
   }
+  if (lane == 0) {
+    max_m[warp] = M;
+    sum_l[warp] = L;
+  }
+#pragma unroll
+  for (int e = 0; e < V; ++e) sum_o[warp][V * lane + e] = acc[e];
+  __syncthreads();
+  const int j = threadIdx.x;
+  if (j >= D) return;
+  M = max_m[0];
+#pragma unroll
+  for (int w = 1; w < kMergeWarps; ++w) M = fmaxf(M, max_m[w]);
+  float x = 0.f;
+  L = 0.f;
+#pragma unroll
+  for (int w = 0; w < kMergeWarps; ++w) {
+    const float f = max_m[w] == -INFINITY ? 0.f : q8_ex2(max_m[w] - M);
+    L = fmaf(f, sum_l[w], L);
+    x = fmaf(f, sum_o[w][j], x);
+  }
+  const int64_t orow = (sp.first + i0 + r / a.G) * a.Hq + static_cast<int64_t>(hk) * a.G + r % a.G;
+  static_cast<T*>(a.out)[orow * D + j] = from_float<T>(L == 0.f ? 0.f : x / L);
 }
 
 }  // namespace axr
