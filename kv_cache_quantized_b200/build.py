@@ -4,7 +4,8 @@
 
 Each translation unit under csrc/ is compiled to an object in _build/ (in parallel), then linked into
 kv_cache_quantized_b200/libaxr.so.  A unit is rebuilt when it or any header in csrc/ or include/ is newer than its
-object.
+object.  binding/axr_torch.cpp becomes the Python extension _axr_torch.so beside it (the paged front end; host code,
+linked against libaxr.so and torch).
 """
 
 from __future__ import annotations
@@ -15,6 +16,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -22,6 +24,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libaxr.so")
+BINDING = os.path.join(PKG, "binding", "axr_torch.cpp")
+EXT = os.path.join(PKG, "_axr_torch.so")
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",
@@ -62,8 +66,29 @@ def _compile(src: str, force: bool, extra: list) -> str:
     return obj
 
 
+def _build_binding(force: bool) -> None:
+    deps = [BINDING, os.path.join(INCLUDE, "axr.h")]
+    if not force and os.path.exists(EXT) and os.path.getmtime(EXT) >= max(os.path.getmtime(d) for d in deps):
+        return
+    import torch
+    root = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
+    tmp = EXT + ".tmp"
+    cmd = [shutil.which("g++") or "g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-I", INCLUDE,
+           "-isystem", os.path.join(root, "include"),
+           "-isystem", os.path.join(root, "include", "torch", "csrc", "api", "include"),
+           "-isystem", os.path.join(cuda, "include"), "-isystem", sysconfig.get_paths()["include"], BINDING, "-o", tmp,
+           "-L", PKG, "-l:libaxr.so", "-Wl,-rpath,$ORIGIN", "-L", os.path.join(root, "lib"), "-lc10", "-lc10_cuda",
+           "-ltorch_cpu", "-ltorch", "-ltorch_python"]
+    res = subprocess.run(cmd, capture_output=True, text=True)
+    if res.returncode != 0:
+        raise RuntimeError(f"g++ failed on {os.path.basename(BINDING)}:\n{res.stderr}")
+    os.replace(tmp, EXT)
+
+
 def build(force: bool = False, jobs: int | None = None, verbose: bool = False, extra: list | None = None) -> str:
-    """Compile every unit and link libaxr.so; returns its path."""
+    """Compile every unit, link libaxr.so and build the paged front end; returns the library's path."""
     os.makedirs(BUILD, exist_ok=True)
     extra = list(extra or [])
     if verbose:
@@ -80,6 +105,7 @@ def build(force: bool = False, jobs: int | None = None, verbose: bool = False, e
         if res.returncode != 0:
             raise RuntimeError(f"link failed:\n{res.stderr}")
         os.replace(tmp, LIB)
+    _build_binding(force)
     return LIB
 
 

@@ -456,95 +456,23 @@ def decode_step_paged(q, k_new, v_new, kcodes, knorms, signs, bits, block_table,
 
 Q8_BLOCK = 16  # tokens that share a scale in the 8-bit cache
 Q8_KINDS = {"i8": _abi.Q8_INT, "e4m3": _abi.Q8_E4M3}
-_DTYPES = {torch.float32: _abi.F32, torch.float16: _abi.F16, torch.bfloat16: _abi.BF16}
 
 
-def _token_rows(name, t, dtype=None):
-    """Element stride between the tokens of t [n_tok, H, d], whose heads are contiguous (a slice of a fused projection
-    row, or a contiguous tensor)."""
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor (libaxr has no CPU path)")
-    if t.dtype not in _DTYPES or (dtype is not None and t.dtype != dtype):
-        raise TypeError(f"{name} must be {dtype or 'float32, float16 or bfloat16'}, got {t.dtype}")
-    if t.dim() != 3:
-        raise ValueError(f"{name} must be [n_tok, heads, d]")
-    n, H, d = t.shape
-    sn, sh, sd = t.stride()
-    if (sd != 1 and d > 1) or (sh != d and H > 1):
-        raise ValueError(f"{name}: the heads of a token must be contiguous")
-    return sn if n > 1 else H * d
+_ext = None
 
 
-def _same_device(ref, *tensors):
-    for t in tensors:
-        if t is not None and t.device != ref.device:
-            raise ValueError(f"tensors on {t.device} and {ref.device}: one device expected")
-
-
-class _on_device:
-    """Makes t's device current for a call (a no-op when it already is)."""
-
-    def __init__(self, t):
-        i = t.device.index
-        self.guard = None if i == torch.cuda.current_device() else torch.cuda.device(i)
-
-    def __enter__(self):
-        if self.guard is not None:
-            self.guard.__enter__()
-
-    def __exit__(self, *exc):
-        if self.guard is not None:
-            self.guard.__exit__(*exc)
-
-
-def _new_tokens(k_new, v_new, q, cos_sin, positions, cu_new, seq_lens, block_table, q_out, q_dtype):
-    """Checks what the two paged append calls share; returns (sizes, the shared leading arguments, q_out)."""
-    ks, vs = _token_rows("k_new", k_new), _token_rows("v_new", v_new, k_new.dtype)
-    n, Hkv, d = k_new.shape
-    if v_new.shape != k_new.shape:
-        raise ValueError("k_new and v_new must have one shape")
-    _need_cuda("block_table", block_table, torch.int32)
-    _need_cuda("seq_lens", seq_lens, torch.int32)
-    if block_table.dim() != 2 or seq_lens.numel() != block_table.shape[0]:
-        raise ValueError("block_table [B, max_blocks] and seq_lens [B] expected")
-    B = block_table.shape[0]
-    if cu_new is not None:
-        _need_cuda("cu_new", cu_new, torch.int32)
-        if cu_new.numel() != B + 1:
-            raise ValueError("cu_new must have B + 1 entries")
-    elif n != B:
-        raise ValueError("without cu_new there is one new token per sequence")
-    if positions is not None:
-        _need_cuda("positions", positions, torch.int32)
-        if positions.numel() != n:
-            raise ValueError("positions must have one entry per new token")
-    max_pos = rot = 0
-    if cos_sin is not None:
-        _need_cuda("cos_sin", cos_sin, torch.float32)
-        if cos_sin.dim() != 2:
-            raise ValueError("cos_sin must be [max_pos, rot]")
-        max_pos, rot = cos_sin.shape
-    Hq = qs = 0
-    if q is not None:
-        if cos_sin is None:
-            raise ValueError("q is taken to be rotated: pass cos_sin")
-        qs = _token_rows("q", q, k_new.dtype)
-        if q.shape[0] != n or q.shape[2] != d:
-            raise ValueError("q must be [n_tok, Hq, d]")
-        Hq = q.shape[1]
-        if q_out is None:
-            q_out = torch.empty((n, Hq, d), dtype=q_dtype, device=q.device)
-        _need_cuda("q_out", q_out, q_dtype)
-        if q_out.shape != q.shape:
-            raise ValueError("q_out must have q's shape")
-    elif q_out is not None:
-        raise ValueError("q_out without q")
-    _same_device(k_new, v_new, q, cos_sin, positions, cu_new, seq_lens, block_table, q_out)
-    lead = (_ptr(q), _ptr(k_new), _ptr(v_new), _DTYPES[k_new.dtype], qs, ks, vs, _ptr(cos_sin), max_pos, rot)
-    mid = (_ptr(positions), _ptr(cu_new), _ptr(seq_lens), n, B, Hq, Hkv, d)
-    return Hkv, d, lead, mid, q_out
+def _paged():
+    """The compiled front end of the paged entry points (binding/axr_torch.cpp)."""
+    global _ext
+    if _ext is None:
+        _abi.lib()
+        try:
+            from . import _axr_torch
+        except ImportError as e:
+            raise RuntimeError("kv_cache_quantized_b200/_axr_torch.so is not built or does not match this torch; run "
+                               "`python -m kv_cache_quantized_b200.build`. There is no CPU fallback.") from e
+        _ext = _axr_torch
+    return _ext
 
 
 def append_paged(k_new, v_new, kcodes, knorms, signs, bits, block_table, seq_lens, cu_new=None, q=None, cos_sin=None,
@@ -557,33 +485,8 @@ def append_paged(k_new, v_new, kcodes, knorms, signs, bits, block_table, seq_len
     into v are stored as float16.  cos_sin [max_pos, rot] float32 holds each position's rot/2 cosines and rot/2 sines;
     pairs are (j, j + rot/2), or (2j, 2j + 1) when interleaved; positions (int32 [n_tok]) overrides the cache positions
     in it.  With q [n_tok, Hq, d], returns the rotated queries [n_tok, Hq, d] float32.  Pools are updated in place."""
-    Hkv, d, lead, mid, q_out = _new_tokens(k_new, v_new, q, cos_sin, positions, cu_new, seq_lens, block_table, q_out,
-                                           torch.float32)
-    _need_cuda("kcodes", kcodes, torch.uint8)
-    _need_cuda("knorms", knorms, torch.float16)
-    _need_cuda("signs", signs, torch.int8)
-    if kcodes.dim() != 4 or kcodes.shape[1] != Hkv or kcodes.shape[3] != row_bytes(d, bits) or \
-            knorms.shape != kcodes.shape[:3] or signs.numel() != d:
-        raise ValueError("kcodes [blocks, Hkv, bt, d*bits/8], knorms [blocks, Hkv, bt], signs [d] expected")
-    vkind, vptr, vnptr = _paged_values(v, vcodes, vnorms, kcodes, knorms, d)
-    _same_device(k_new, kcodes, knorms, signs, v, vcodes, vnorms)
-    with _on_device(k_new):
-        st = _abi.lib().axr_append_paged(*lead, 1 if interleaved else 0, *mid, bits, _ptr(signs), _ptr(kcodes),
-                                         _ptr(knorms), vkind, vptr, vnptr, _ptr(block_table), block_table.shape[1],
-                                         kcodes.shape[2], kcodes.shape[0], _ptr(q_out), _stream())
-    _abi.check(st, "axr_append_paged")
-    return q_out
-
-
-def _q8_pools(kcodes, kscales, vcodes, vscales):
-    for name, c, s in (("k", kcodes, kscales), ("v", vcodes, vscales)):
-        _need_cuda(name + "codes", c, torch.uint8)
-        _need_cuda(name + "scales", s, torch.float32)
-        if c.dim() != 4 or c.shape[2] % Q8_BLOCK or tuple(s.shape) != (c.shape[0], c.shape[1], c.shape[2] // Q8_BLOCK):
-            raise ValueError(f"{name}codes [blocks, Hkv, bt, d], {name}scales [blocks, Hkv, bt/16] expected")
-    if vcodes.shape != kcodes.shape:
-        raise ValueError("vcodes must have kcodes' shape")
-    return kcodes.shape
+    return (_ext or _paged()).append_paged(k_new, v_new, kcodes, knorms, signs, bits, block_table, seq_lens, cu_new, q,
+                                           cos_sin, positions, interleaved, v, vcodes, vnorms, q_out)
 
 
 def _q8_kind(kind):
@@ -599,19 +502,8 @@ def q8_append_paged(k_new, v_new, kcodes, kscales, vcodes, vscales, block_table,
     Codes [blocks, Hkv, bt, d] uint8 hold int8 integers (kind "i8") or e4m3 floats ("e4m3"); scales [blocks, Hkv, bt/16]
     float32 one factor for each 16 tokens and head.  A block's scale is the largest that its tokens have needed; when it
     grows, the codes of its older tokens are rounded again.  With q, returns the rotated queries in q's dtype."""
-    kd = _q8_kind(kind)
-    Hkv, d, lead, mid, q_out = _new_tokens(k_new, v_new, q, cos_sin, positions, cu_new, seq_lens, block_table, q_out,
-                                           k_new.dtype)
-    nb, H, bt, dd = _q8_pools(kcodes, kscales, vcodes, vscales)
-    if H != Hkv or dd != d:
-        raise ValueError("the pools do not match the new tokens' heads")
-    _same_device(k_new, kcodes, kscales, vcodes, vscales)
-    with _on_device(k_new):
-        st = _abi.lib().axr_q8_append_paged(*lead, 1 if interleaved else 0, *mid, kd, _ptr(kcodes), _ptr(kscales),
-                                            _ptr(vcodes), _ptr(vscales), _ptr(block_table), block_table.shape[1], bt,
-                                            nb, _ptr(q_out), _stream())
-    _abi.check(st, "axr_q8_append_paged")
-    return q_out
+    return (_ext or _paged()).q8_append_paged(k_new, v_new, kcodes, kscales, vcodes, vscales, block_table, seq_lens,
+                                              _q8_kind(kind), cu_new, q, cos_sin, positions, interleaved, q_out)
 
 
 def q8_attend_workspace_bytes(n_tok, max_q, B, Hq, Hkv, T, d) -> int:
@@ -626,43 +518,8 @@ def q8_attend_paged(q, kcodes, kscales, vcodes, vscales, block_table, seq_lens=N
     cu_q[b] .. cu_q[b+1] - 1 (int32 [B+1]; None: one per sequence, a decode step), the last positions of its seq_lens[b];
     each sees the cache up to its own position.  max_q (optional) bounds a sequence's query tokens, T (default
     max_blocks * bt) its length.  Returns out [n_tok, Hq, d] in q's dtype."""
-    kd = _q8_kind(kind)
-    qs = _token_rows("q", q)
-    n, Hq, d = q.shape
-    nb, Hkv, bt, dd = _q8_pools(kcodes, kscales, vcodes, vscales)
-    if dd != d:
-        raise ValueError("the pools do not match q's head dimension")
-    _need_cuda("block_table", block_table, torch.int32)
-    if block_table.dim() != 2:
-        raise ValueError("block_table must be [B, max_blocks]")
-    B, mb = block_table.shape
-    seq_lens = _lens(seq_lens, B)
-    if cu_q is not None:
-        _need_cuda("cu_q", cu_q, torch.int32)
-        if cu_q.numel() != B + 1:
-            raise ValueError("cu_q must have B + 1 entries")
-        max_q = 0 if max_q is None else int(max_q)
-    else:
-        if n != B:
-            raise ValueError("without cu_q there is one query token per sequence")
-        max_q = 1
-    T = mb * bt if T is None else int(T)
-    scale = 1.0 / math.sqrt(d) if scale is None else float(scale)
-    if out is None:
-        out = torch.empty((n, Hq, d), dtype=q.dtype, device=q.device)
-    _need_cuda("out", out, q.dtype)
-    if tuple(out.shape) != (n, Hq, d):
-        raise ValueError("out must be [n_tok, Hq, d]")
-    _same_device(q, kcodes, kscales, vcodes, vscales, block_table, seq_lens, cu_q, out, workspace)
-    nbytes = q8_attend_workspace_bytes(n, max_q, B, Hq, Hkv, T, d)
-    ws = _workspace(nbytes, q.device, workspace) if nbytes or workspace is not None else None
-    with _on_device(q):
-        st = _abi.lib().axr_q8_attend_paged(_ptr(q), _DTYPES[q.dtype], qs, _ptr(kcodes), _ptr(kscales), _ptr(vcodes),
-                                            _ptr(vscales), kd, _ptr(block_table), mb, bt, nb, _ptr(cu_q),
-                                            _ptr(seq_lens), n, max_q, B, Hq, Hkv, T, d, scale, _ptr(out), _ptr(ws),
-                                            0 if ws is None else ws.numel(), _stream())
-    _abi.check(st, "axr_q8_attend_paged")
-    return out
+    return (_ext or _paged()).q8_attend_paged(q, kcodes, kscales, vcodes, vscales, block_table, seq_lens,
+                                              _q8_kind(kind), cu_q, max_q, T, scale, out, workspace)
 
 
 # ---- LOOKAT product quantization ------------------------------------------------------------------------------------
