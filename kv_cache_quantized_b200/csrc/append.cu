@@ -1,10 +1,13 @@
 // axr_append_paged: new tokens of a ragged batch rotated, quantized with the Lloyd-Max codebook (write_vec.cuh) and
 // written into paged pools through the block table; queries rotated into fp32 rows for the decode entry points.
 //
-// One thread block per token; every warp takes key heads, value heads and query rows in turn.  Keys and values keep
-// the writer kernels' layout (d / 32 coordinates a lane, so that the Walsh-Hadamard butterfly runs in registers),
-// queries 8 coordinates a lane.  The codes equal axr_write_keys' for the rotated key, bit for bit: the same
-// quantize_lane on the same fp32 values.  HBM traffic bounds it on long chunks, launch latency on single tokens.
+// Every warp works alone: on a token and KH of its key and value heads, or on a token and a slice of its query rows
+// (rotate_queries).  Keys and values keep the writer kernels' layout (d / 32 coordinates a lane, so that the
+// Walsh-Hadamard butterfly runs in registers), queries 8 coordinates a lane; a warp's rows are all on their way before
+// its token's place in the cache is known.  The codes equal axr_write_keys' for the rotated key, bit for bit: the same
+// quantize_lane on the same fp32 values.  KH = 4 keeps 2 KB a warp in flight on long calls; short calls take KH = 1, a
+// head a warp.  Issue slots bound the quantized heads (about 250 instructions a vector), HBM traffic the query and fp16
+// value rows, launch latency single tokens.
 #include "axr_host.h"
 #include "paged_host.h"
 #include "paged_new.cuh"
@@ -26,108 +29,98 @@ struct AppendArgs {
   Codebook cb;
 };
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;
 constexpr int kWarps = kThreads / 32;
 
-// Codes of one row to its place: lanes hold whole bytes of the bitstream when d / 32 codes fill them, else the row is
-// packed through shared memory.
+// Codes of one row to its place.  A lane holds N = BITS d / 32 consecutive bits of the row's bitstream: whole bytes are
+// stored as they are; otherwise groups of lanes that fill BITS (or 1) 32-bit words OR their fields together.
 template <int D, int BITS>
-__device__ __forceinline__ void store_codes(const int (&code)[D / 32], uint8_t* __restrict__ out, int lane,
-                                            uint8_t* scratch) {
+__device__ __forceinline__ void store_codes(const int (&code)[D / 32], uint8_t* __restrict__ out, int lane) {
   constexpr int VPL = D / 32, N = VPL * BITS;
-  if constexpr (N == 8 || N == 16) {
-    uint32_t w = 0;
+  uint32_t f = 0;
 #pragma unroll
-    for (int i = 0; i < VPL; ++i) w |= static_cast<uint32_t>(code[i]) << (i * BITS);
-    if constexpr (N == 8) out[lane] = static_cast<uint8_t>(w);
-    else reinterpret_cast<uint16_t*>(out)[lane] = static_cast<uint16_t>(w);
+  for (int i = 0; i < VPL; ++i) f |= static_cast<uint32_t>(code[i]) << (i * BITS);
+  if constexpr (N == 8) {
+    out[lane] = static_cast<uint8_t>(f);
+  } else if constexpr (N == 16) {
+    reinterpret_cast<uint16_t*>(out)[lane] = static_cast<uint16_t>(f);
   } else {
-    __syncwarp();  // the previous row's bytes are read
+    constexpr int W = N % 3 == 0 ? 3 : 1;      // words of a group
+    constexpr int GL = 32 * W / N;             // its lanes
+    static_assert(GL * N == 32 * W && (GL & (GL - 1)) == 0, "whole words from a power of two of lanes");
+    const int pos = (lane & (GL - 1)) * N;
+    const uint64_t at = static_cast<uint64_t>(f) << (pos & 31);
+    uint32_t w[W];
 #pragma unroll
-    for (int i = 0; i < VPL; ++i) scratch[lane * VPL + i] = static_cast<uint8_t>(code[i]);
-    __syncwarp();
-    pack_row<D, BITS>(scratch, out, lane);
+    for (int k = 0; k < W; ++k)
+      w[k] = pos >> 5 == k ? static_cast<uint32_t>(at) : (pos >> 5) + 1 == k ? static_cast<uint32_t>(at >> 32) : 0u;
+#pragma unroll
+    for (int m = 1; m < GL; m <<= 1)
+#pragma unroll
+      for (int k = 0; k < W; ++k) w[k] |= __shfl_xor_sync(0xffffffffu, w[k], m);
+    const int mine = lane & (GL - 1);
+    uint32_t x = w[0];
+#pragma unroll
+    for (int k = 1; k < W; ++k) x = mine == k ? w[k] : x;
+    if (mine < W) reinterpret_cast<uint32_t*>(out)[lane / GL * W + mine] = x;
   }
 }
 
-template <typename T, int D, int BITS, bool VQ>
+// Units of work: kv_units of (token, KH KV heads), then (token, slice of query heads).
+template <typename T, int D, int BITS, bool VQ, int KH>
 __global__ void __launch_bounds__(kThreads)
-append_kernel(const __grid_constant__ PagedNew p, const __grid_constant__ AppendArgs a) {
-  constexpr int VPL = D / 32, R = D * BITS / 8, LPR = D / 8, RPW = 32 / LPR;
-  __shared__ uint8_t scratch[kWarps][D];
+append_kernel(const __grid_constant__ PagedNew p, const __grid_constant__ AppendArgs a, int64_t kv_units, int kv_parts,
+              int q_parts) {
+  constexpr int VPL = D / 32, R = D * BITS / 8;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int64_t tok = blockIdx.x;
-  int b = static_cast<int>(tok);
-  if (p.cu) b = last_at_most(p.B, tok, lane, [&](int s) { return static_cast<int64_t>(p.cu[s]); });
-  const NewSpan sp = new_span(p, b);
-  if (tok < sp.first || tok >= sp.first + sp.count) return;  // a token past the last sequence
-  const int64_t pos64 = static_cast<int64_t>(sp.pos0) + (tok - sp.first);
-  if (pos64 < 0) return;
-  const int64_t rpos = p.positions ? static_cast<int64_t>(p.positions[tok]) : pos64;
-  int64_t row = -1;
-  if (pos64 < sp.len && !(p.cos_sin && (rpos < 0 || rpos >= p.max_pos)))
-    row = page_row(p, b, static_cast<int>(pos64), a.Hkv);
-  if (row < 0) {
-    if (threadIdx.x == 0) atomicOr(p.status, kStatusBadIndex);
-    return;  // uniform over the block
+  const int64_t unit = static_cast<int64_t>(blockIdx.x) * kWarps + warp;
+  if (unit >= kv_units) {
+    const int64_t u = unit - kv_units;
+    if (q_parts == 0 || u >= p.n_tok * q_parts) return;
+    rotate_queries<T, float, D>(p, a.q, a.q_stride, a.q_out, a.Hq, a.Hkv, u / q_parts, static_cast<int>(u % q_parts),
+                                lane);
+    return;
   }
-  row += pos64 & ((1 << p.shift) - 1);
-
-  if (a.q) {
-    Turn<8> t;
-    const int e0 = 8 * (lane % LPR);
-    t.load(p, rpos, e0, true);
-    const T* src = static_cast<const T*>(a.q) + tok * a.q_stride + e0;
-    float* dst = a.q_out + tok * a.Hq * D + e0;
-    constexpr int U = 2;
-    for (int h0 = warp * RPW; h0 < a.Hq; h0 += kWarps * RPW * U) {
-      Raw8<T> r[U];
+  const int64_t tok = unit / kv_parts;
+  const int h0 = static_cast<int>(unit % kv_parts) * KH;
+  const T* ks = static_cast<const T*>(a.k) + tok * a.k_stride + static_cast<int64_t>(h0) * D;
+  const T* vs = static_cast<const T*>(a.v) + tok * a.v_stride + static_cast<int64_t>(h0) * D;
+  float x[KH][VPL], y[KH][VPL];
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int h = h0 + u * kWarps * RPW + lane / LPR;
-        if (h < a.Hq) r[u].load(src + static_cast<int64_t>(h) * D);
-        else r[u].zero();
-      }
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int h = h0 + u * kWarps * RPW + lane / LPR;
-        float x[8], o[8];
-        r[u].values(x);
-        r[u].from_lane(lane + t.partner).values(o);
-        t.apply(x, o);
-        if (h < a.Hq) store8(dst + static_cast<int64_t>(h) * D, x);
-      }
-    }
+  for (int i = 0; i < KH; ++i) {
+    const bool on = h0 + i < a.Hkv;
+    load_lane<T, VPL>(ks + (on ? i * D : 0), lane, x[i]);
+    load_lane<T, VPL>(vs + (on ? i * D : 0), lane, y[i]);
   }
-
   float sg[VPL], tau[(1 << BITS) - 1];
 #pragma unroll
   for (int i = 0; i < VPL; ++i) sg[i] = sign_of(a.signs[lane * VPL + i]);
 #pragma unroll
   for (int k = 0; k < (1 << BITS) - 1; ++k) tau[k] = a.cb.tau[k];
+  const NewPlace at = place_of(p, tok, lane, a.Hkv);
+  if (!at.ok) return;  // uniform over the warp
   Turn<VPL> t;
-  t.load(p, rpos, lane * VPL, true);
-  for (int h = warp; h < a.Hkv; h += kWarps) {
-    const int64_t r = row + (static_cast<int64_t>(h) << p.shift);
-    float x[VPL], y[VPL];
-    load_lane<T, VPL>(static_cast<const T*>(a.k) + tok * a.k_stride + static_cast<int64_t>(h) * D, lane, x);
-    load_lane<T, VPL>(static_cast<const T*>(a.v) + tok * a.v_stride + static_cast<int64_t>(h) * D, lane, y);
+  t.load(p, at.rpos, lane * VPL, true);
+#pragma unroll
+  for (int j = 0; j < KH; ++j) {
+    if (h0 + j >= a.Hkv) break;
+    const int64_t r = at.row + (static_cast<int64_t>(h0 + j) << p.shift);
     float o[VPL];
 #pragma unroll
-    for (int i = 0; i < VPL; ++i) o[i] = __shfl_sync(0xffffffffu, x[i], lane + t.partner);
-    t.apply(x, o);
+    for (int i = 0; i < VPL; ++i) o[i] = __shfl_sync(0xffffffffu, x[j][i], lane + t.partner);
+    t.apply(x[j], o);
     int code[VPL];
-    const float n = quantize_lane<D, BITS>(x, sg, tau, lane, code);
-    store_codes<D, BITS>(code, a.kcodes + r * R, lane, scratch[warp]);
+    const float n = quantize_lane<D, BITS>(x[j], sg, tau, lane, code);
+    store_codes<D, BITS>(code, a.kcodes + r * R, lane);
     if (lane == 0) a.knorms[r] = __float2half_rn(n);
     if constexpr (VQ) {
-      const float nv = quantize_lane<D, BITS>(y, sg, tau, lane, code);
-      store_codes<D, BITS>(code, static_cast<uint8_t*>(a.vals) + r * R, lane, scratch[warp]);
+      const float nv = quantize_lane<D, BITS>(y[j], sg, tau, lane, code);
+      store_codes<D, BITS>(code, static_cast<uint8_t*>(a.vals) + r * R, lane);
       if (lane == 0) a.vnorms[r] = __float2half_rn(nv);
     } else {
       __half2 w[VPL / 2];  // fp16 inputs are stored as they are, others rounded to nearest even
 #pragma unroll
-      for (int i = 0; i < VPL; i += 2) w[i / 2] = __floats2half2_rn(y[i], y[i + 1]);
+      for (int i = 0; i < VPL; i += 2) w[i / 2] = __floats2half2_rn(y[j][i], y[j][i + 1]);
       __half* dst = static_cast<__half*>(a.vals) + r * D + lane * VPL;
       if constexpr (VPL == 4) *reinterpret_cast<uint2*>(dst) = *reinterpret_cast<const uint2*>(w);
       else *reinterpret_cast<__half2*>(dst) = w[0];
@@ -135,12 +128,23 @@ append_kernel(const __grid_constant__ PagedNew p, const __grid_constant__ Append
   }
 }
 
+template <typename T, int D, int BITS, bool VQ, int KH>
+axr_status launch_kh(const PagedNew& p, const AppendArgs& a, cudaStream_t st, const char* w) {
+  const int kv_parts = (a.Hkv + KH - 1) / KH, q_parts = a.q ? (a.Hq + query_slice(D) - 1) / query_slice(D) : 0;
+  const int64_t kv_units = p.n_tok * kv_parts, units = kv_units + p.n_tok * q_parts;
+  const int64_t grid = (units + kWarps - 1) / kWarps;
+  if (grid > 0x7fffffff) return set_error(AXR_EUNSUPPORTED, "%s: too many tokens and heads for one call", w);
+  append_kernel<T, D, BITS, VQ, KH>
+      <<<static_cast<unsigned>(grid), kThreads, 0, st>>>(p, a, kv_units, kv_parts, q_parts);
+  return check_launch(w);
+}
+
 template <typename T, int D, int BITS>
 axr_status launch(bool vq, const PagedNew& p, const AppendArgs& a, cudaStream_t st, const char* w) {
-  const unsigned grid = static_cast<unsigned>(p.n_tok);
-  if (vq) append_kernel<T, D, BITS, true><<<grid, kThreads, 0, st>>>(p, a);
-  else append_kernel<T, D, BITS, false><<<grid, kThreads, 0, st>>>(p, a);
-  return check_launch(w);
+  // a head a warp until the warps fill the SMs twice over (about 24 resident a SM)
+  const bool wide = p.n_tok * a.Hkv > static_cast<int64_t>(kSmCount) * 48;
+  if (vq) return wide ? launch_kh<T, D, BITS, true, 4>(p, a, st, w) : launch_kh<T, D, BITS, true, 1>(p, a, st, w);
+  return wide ? launch_kh<T, D, BITS, false, 4>(p, a, st, w) : launch_kh<T, D, BITS, false, 1>(p, a, st, w);
 }
 
 template <typename T, int D>

@@ -86,11 +86,11 @@ __device__ __forceinline__ void fwht_warp(float (&v)[WarpVec<D>::VPL], int lane)
   // stages across lanes: element stride h = m * VPL for lane mask m
 #pragma unroll
   for (int m = 1; m < WarpVec<D>::LANES; m <<= 1) {
-    const bool upper = (lane & m) != 0;
+    const float sgn = (lane & m) != 0 ? -1.0f : 1.0f;
 #pragma unroll
     for (int i = 0; i < VPL; ++i) {
-      float other = __shfl_xor_sync(0xffffffffu, v[i], m);
-      v[i] = upper ? (other - v[i]) : (v[i] + other);
+      const float other = __shfl_xor_sync(0xffffffffu, v[i], m);
+      v[i] = fmaf(v[i], sgn, other);  // other + v or other - v, rounded once
     }
   }
 }

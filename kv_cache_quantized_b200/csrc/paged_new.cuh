@@ -46,22 +46,44 @@ __device__ __forceinline__ int last_at_most(int B, int64_t key, int lane, First 
 struct NewSpan {
   int64_t first;
   int count, pos0, len;
+  bool cut;  // the length passes the block table's reach: what lies past it is skipped
 };
 
-__device__ __forceinline__ NewSpan new_span(const PagedNew& p, int b) {
-  NewSpan s;
+// The span of the last sequence b with first(cu[b], b) <= key, where first is non-decreasing in b; without cu, of
+// sequence `key`.  One warp; each lane holds one sequence's entries a round, so that finding a sequence and reading its
+// entries is one round trip to memory for every 32 sequences, all in flight together.
+template <class First>
+__device__ __forceinline__ NewSpan find_span(const PagedNew& p, int64_t key, int lane, int& b, First first) {
   const int cap = p.max_blocks << p.shift;
-  s.len = p.seq_lens[b];
-  int64_t lo = b, hi = static_cast<int64_t>(b) + 1;
+  NewSpan s;
+  int lo = 0, hi = 0, len = 0;
   if (p.cu) {
-    lo = p.cu[b];
-    hi = p.cu[b + 1];
+    b = 0;
+#pragma unroll 2
+    for (int b0 = 0; b0 < p.B; b0 += 32) {
+      const int c = min(b0 + lane, p.B - 1);
+      const int l = p.cu[c], h = p.cu[c + 1], n = p.seq_lens[c];
+      const unsigned who = __ballot_sync(0xffffffffu, b0 + lane < p.B && first(l, c) <= key);
+      if (who || b0 == 0) {
+        const int src = who ? 31 - __clz(who) : 0;
+        b = b0 + src;
+        lo = __shfl_sync(0xffffffffu, l, src);
+        hi = __shfl_sync(0xffffffffu, h, src);
+        len = __shfl_sync(0xffffffffu, n, src);
+      }
+    }
+    if (lo < 0 || hi > p.n_tok || hi < lo) lo = hi = 0;  // an inconsistent table has no new tokens here
+  } else {
+    b = static_cast<int>(key);
+    lo = b;
+    hi = b + 1;
+    len = p.seq_lens[b];
   }
-  if (lo < 0 || hi > p.n_tok || hi < lo) lo = hi = 0;  // an inconsistent table has no new tokens here
   s.first = lo;
-  s.count = static_cast<int>(hi - lo);
-  s.pos0 = s.len - s.count;
-  if (s.len > cap) s.len = cap;  // what lies past the table's reach is skipped (and flagged by the caller)
+  s.count = hi - lo;
+  s.pos0 = len - s.count;
+  s.cut = len > cap;
+  s.len = s.cut ? cap : len;
   return s;
 }
 
@@ -215,5 +237,62 @@ struct Turn {
     for (int i = 0; i < N; ++i) v[i] = y[i];
   }
 };
+
+// A new token's place: its sequence's pool row (token row of its block, KV head 0) and rotation position.
+struct NewPlace {
+  int64_t row, rpos;
+  bool ok;
+};
+
+// One warp.  Tokens without a sequence or with a negative position are not ok; tokens whose table entry, position or
+// rotation position is out of range are not ok either and set the status word.
+__device__ __forceinline__ NewPlace place_of(const PagedNew& p, int64_t tok, int lane, int Hkv) {
+  NewPlace r{-1, 0, false};
+  int b;
+  const NewSpan sp = find_span(p, tok, lane, b, [](int first, int) { return static_cast<int64_t>(first); });
+  const int64_t pos = static_cast<int64_t>(sp.pos0) + (tok - sp.first);
+  if (tok < sp.first || tok >= sp.first + sp.count || pos < 0) return r;
+  r.rpos = p.positions ? static_cast<int64_t>(p.positions[tok]) : pos;
+  r.ok = pos < sp.len && !(p.cos_sin && (r.rpos < 0 || r.rpos >= p.max_pos));
+  if (r.ok) {
+    r.row = page_row(p, b, static_cast<int>(pos), Hkv);
+    r.ok = r.row >= 0;
+    r.row += pos & ((1 << p.shift) - 1);
+  }
+  if (!r.ok && lane == 0) atomicOr(p.status, kStatusBadIndex);
+  return r;
+}
+
+// Query rows of a token rotated by one warp: slice `part` of its heads, kQuerySlice(D) of them, 8 coordinates a lane,
+// U rows a lane group.  The rows are on their way before the token's place is known.
+constexpr int kQueryRows = 8;
+__host__ __device__ constexpr int query_slice(int D) { return kQueryRows * (256 / D); }
+
+template <typename T, typename TO, int D>
+__device__ __forceinline__ void rotate_queries(const PagedNew& p, const void* q, int64_t q_stride, void* q_out, int Hq,
+                                               int Hkv, int64_t tok, int part, int lane) {
+  constexpr int U = kQueryRows, LPR = D / 8, RPW = 32 / LPR;
+  const int e0 = 8 * (lane % LPR), h0 = part * query_slice(D) + lane / LPR;
+  const T* src = static_cast<const T*>(q) + tok * q_stride + e0;
+  TO* dst = static_cast<TO*>(q_out) + tok * Hq * D + e0;
+  Raw8<T> r[U];
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    if (h0 + u * RPW < Hq) r[u].load(src + static_cast<int64_t>(h0 + u * RPW) * D);
+    else r[u].zero();
+  }
+  const NewPlace at = place_of(p, tok, lane, Hkv);
+  if (!at.ok) return;  // uniform over the warp
+  Turn<8> t;
+  t.load(p, at.rpos, e0, true);
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    float x[8], o[8];
+    r[u].values(x);
+    r[u].from_lane(lane + t.partner).values(o);
+    t.apply(x, o);
+    if (h0 + u * RPW < Hq) store8(dst + static_cast<int64_t>(h0 + u * RPW) * D, x);
+  }
+}
 
 }  // namespace axr

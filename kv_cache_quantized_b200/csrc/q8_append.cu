@@ -1,12 +1,13 @@
 // axr_q8_append_paged: new tokens rotated, quantized to 8 bits and written through the block table; queries rotated.
 //
-// One thread block takes one 16-token scale block of a sequence and up to HPC KV heads of it, with their query heads.
-// Every lane holds 8 consecutive coordinates of one token row, so a warp load is 16 bytes a lane and a row's rotation
-// factors are loaded once and serve all its heads.  The block's largest magnitude goes through one redux per warp and
-// head and a shared-memory maximum; then
+// One thread block takes one 16-token scale block of a sequence and up to HPC KV heads; further blocks rotate the queries
+// (rotate_queries, a warp a token and slice of heads).  Every lane holds 8 consecutive coordinates of one token row, so
+// a warp load is 16 bytes a lane and a row's rotation factors are loaded once and serve all its heads.  The scale
+// block's largest magnitude goes through one redux per warp and head and a shared-memory maximum; then
 //   s = max(s_old, need(amax)),  code = rne(x * (1 / s)),  and, where s grew, older codes = rne(code * (s_old * (1 / s)))
 // so a scale block is one work item, whatever mix of older and new tokens it holds, and no atomics on global memory
-// are needed.  HBM traffic bounds it: q, k and v are read once and q, codes and scales written once.
+// are needed.  HBM traffic bounds long calls: q, k and v are read once and q, codes and scales written once; a step of
+// single tokens is three round trips to memory (the sequence's entries; its table entry, rows and rotation; the scales).
 #include "axr_host.h"
 #include "paged_new.cuh"
 #include "paged_host.h"
@@ -65,34 +66,41 @@ __device__ __forceinline__ void q8_store(uint8_t* dst, const float (&x)[8], floa
 }
 
 template <typename T, int D, bool I8>
-__global__ void __launch_bounds__(kAppendThreads)
-q8_append_kernel(const __grid_constant__ PagedNew p, const __grid_constant__ Q8AppendArgs a) {
+__global__ void __launch_bounds__(kAppendThreads, 3)
+q8_append_kernel(const __grid_constant__ PagedNew p, const __grid_constant__ Q8AppendArgs a, int64_t kv_blocks,
+                 int kv_parts, int q_parts) {
   using P = Q8AppendPlan<D>;
   constexpr int NH = kHeadsPerWarp;
   __shared__ unsigned int amax_s[2][P::HPC];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int sub = lane / P::LPR, e0 = 8 * (lane % P::LPR);
 
-  // the item's sequence and scale block
-  int b = blockIdx.x, j = 0;
-  if (p.cu) {
-    auto start = [&](int s) { return static_cast<int64_t>(p.cu[s] >> 4) + 2 * s; };
-    b = last_at_most(p.B, blockIdx.x, lane, start);
-    j = static_cast<int>(blockIdx.x - start(b));
+  if (blockIdx.x >= kv_blocks) {
+    const int64_t u = (blockIdx.x - kv_blocks) * (kAppendThreads / 32) + warp;
+    if (q_parts == 0 || u >= p.n_tok * q_parts) return;
+    rotate_queries<T, T, D>(p, a.q, a.q_stride, a.q_out, a.Hq, a.Hkv, u / q_parts, static_cast<int>(u % q_parts), lane);
+    return;
   }
-  const NewSpan sp = new_span(p, b);
-  if (threadIdx.x < 2 * P::HPC) (&amax_s[0][0])[threadIdx.x] = 0u;
+  // the item's sequence and scale block, and the block's KV heads
+  const int64_t item = static_cast<int64_t>(blockIdx.x) / kv_parts;
+  const int part = static_cast<int>(blockIdx.x % kv_parts);
+  int b;
+  auto start = [](int first, int s) { return static_cast<int64_t>(first >> 4) + 2 * s; };
+  const NewSpan sp = find_span(p, item, lane, b, start);
+  const int j = p.cu ? static_cast<int>(item - start(static_cast<int>(sp.first), b)) : 0;
   const int lo = max(sp.pos0, 0);
   const int64_t blk64 = static_cast<int64_t>(lo >> 4) + j;
-  if (j < 0 || sp.count == 0 || lo >= sp.len || blk64 * kQ8Block >= sp.len) {
-    if (j == 0 && sp.count > 0 && p.seq_lens[b] > sp.len && threadIdx.x == 0) atomicOr(p.status, kStatusBadIndex);
-    return;  // uniform over the block
-  }
+  if (threadIdx.x == 0 && sp.cut && sp.count > 0) atomicOr(p.status, kStatusBadIndex);
+  if (j < 0 || sp.count == 0 || lo >= sp.len || blk64 * kQ8Block >= sp.len) return;  // uniform over the block
   const int t_blk = static_cast<int>(blk64) * kQ8Block;
   const int64_t row0 = page_row(p, b, t_blk, a.Hkv);
-  if (threadIdx.x == 0 && (row0 < 0 || p.seq_lens[b] > sp.len)) atomicOr(p.status, kStatusBadIndex);
-  if (row0 < 0) return;
+  if (row0 < 0) {
+    if (threadIdx.x == 0) atomicOr(p.status, kStatusBadIndex);
+    return;
+  }
   const int off0 = t_blk & ((1 << p.shift) - 1);
+
+  if (threadIdx.x < 2 * P::HPC) (&amax_s[0][0])[threadIdx.x] = 0u;
 
   // keys and values: this lane's token, NH heads
   const int slot = (warp % P::TW) * P::RPW + sub, pos = t_blk + slot;
@@ -108,7 +116,7 @@ q8_append_kernel(const __grid_constant__ PagedNew p, const __grid_constant__ Q8A
     }
   }
   const int hl0 = (warp / P::TW) * NH;                 // first head, of the block's
-  const int h0 = static_cast<int>(blockIdx.y) * P::HPC + hl0;
+  const int h0 = part * P::HPC + hl0;
   Raw8<T> kr[NH], vr[NH];
   float ks_old[NH], vs_old[NH];
 #pragma unroll
@@ -131,43 +139,6 @@ q8_append_kernel(const __grid_constant__ PagedNew p, const __grid_constant__ Q8A
   Turn<8> turn;
   turn.load(p, rpos, e0, is_new);
   __syncthreads();  // amax_s is zero
-
-  // queries: the block's new tokens x its query heads, dealt over all rows in flight
-  if (a.q) {
-    const int G = a.Hq / a.Hkv;
-    const int hq0 = static_cast<int>(blockIdx.y) * P::HPC * G;
-    const int nq = min(a.Hq, hq0 + P::HPC * G) - hq0;
-    const int n0 = max(sp.pos0 - t_blk, 0), nv = min(sp.len - t_blk, kQ8Block) - n0;  // nv >= 1
-    const int grp = warp * P::RPW + sub;
-    const int step = P::GROUPS / nv, hs = grp / nv;
-    const int qpos = t_blk + n0 + grp % nv;
-    const int64_t qtok = sp.first + (qpos - sp.pos0);
-    int64_t qr = p.positions ? static_cast<int64_t>(p.positions[qtok]) : qpos;
-    const bool live = hs < step && !(p.cos_sin && (qr < 0 || qr >= p.max_pos));
-    Turn<8> tq;
-    tq.load(p, qr, e0, live);
-    const T* src = static_cast<const T*>(a.q) + qtok * a.q_stride + static_cast<int64_t>(hq0) * D + e0;
-    T* dst = static_cast<T*>(a.q_out) + (qtok * a.Hq + hq0) * D + e0;
-    constexpr int U = sizeof(T) == 4 ? 2 : 4;
-    for (int i0 = 0; i0 * step < nq; i0 += U) {
-      Raw8<T> r[U];
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int h = hs + (i0 + u) * step;
-        if (live && h < nq) r[u].load(src + static_cast<int64_t>(h) * D);
-        else r[u].zero();
-      }
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int h = hs + (i0 + u) * step;
-        float x[8], o[8];
-        r[u].values(x);
-        r[u].from_lane(lane + tq.partner).values(o);
-        tq.apply(x, o);
-        if (live && h < nq) store8(dst + static_cast<int64_t>(h) * D, x);
-      }
-    }
-  }
 
   float kx[NH][8];
 #pragma unroll
@@ -212,10 +183,14 @@ q8_append_kernel(const __grid_constant__ PagedNew p, const __grid_constant__ Q8A
 template <typename T, int D>
 axr_status launch(bool i8, const PagedNew& p, const Q8AppendArgs& a, cudaStream_t st, const char* w) {
   const int64_t items = p.cu ? (p.n_tok >> 4) + 2 * static_cast<int64_t>(p.B) : p.B;
-  const dim3 grid(static_cast<unsigned>(items), static_cast<unsigned>((a.Hkv + Q8AppendPlan<D>::HPC - 1) /
-                                                                      Q8AppendPlan<D>::HPC));
-  if (i8) q8_append_kernel<T, D, true><<<grid, kAppendThreads, 0, st>>>(p, a);
-  else q8_append_kernel<T, D, false><<<grid, kAppendThreads, 0, st>>>(p, a);
+  constexpr int warps = kAppendThreads / 32;
+  const int kv_parts = (a.Hkv + Q8AppendPlan<D>::HPC - 1) / Q8AppendPlan<D>::HPC;
+  const int q_parts = a.q ? (a.Hq + query_slice(D) - 1) / query_slice(D) : 0;
+  const int64_t kv_blocks = items * kv_parts, grid = kv_blocks + (p.n_tok * q_parts + warps - 1) / warps;
+  if (grid > 0x7fffffff) return set_error(AXR_EUNSUPPORTED, "%s: too many tokens and heads for one call", w);
+  const unsigned g = static_cast<unsigned>(grid);
+  if (i8) q8_append_kernel<T, D, true><<<g, kAppendThreads, 0, st>>>(p, a, kv_blocks, kv_parts, q_parts);
+  else q8_append_kernel<T, D, false><<<g, kAppendThreads, 0, st>>>(p, a, kv_blocks, kv_parts, q_parts);
   return check_launch(w);
 }
 

@@ -60,13 +60,26 @@ __device__ __forceinline__ void load_lane<__nv_bfloat16, 2>(const __nv_bfloat16*
   v[0] = a.x; v[1] = a.y;
 }
 
+// Number of the L - 1 thresholds at or below w.  The thresholds are symmetric about the middle one, 0: the L / 2 - 1
+// positive ones are counted against |w| (w < 0 lies at or above -t exactly when |w| <= t, so its |w| counts from the
+// next smaller float), half the comparisons of the full count and the same result.
+template <int BITS>
+__device__ __forceinline__ int level_of(float w, const float (&tau)[(1 << BITS) - 1]) {
+  constexpr int L = 1 << BITS, H = L / 2;
+  const bool neg = w < 0.f;
+  const float a = __int_as_float(__float_as_int(fabsf(w)) - (neg ? 1 : 0));
+  int n = 0;
+#pragma unroll
+  for (int k = 0; k < H - 1; ++k) n += (a >= tau[H + k]) ? 1 : 0;
+  return w != w ? 0 : neg ? H - 1 - n : H + n;  // a NaN is at or above no threshold
+}
+
 // The lane's coordinates v (lanes below LANES; zeros elsewhere) to its codes q; returns ||x||.  Whole warp.
 template <int D, int BITS>
 __device__ __forceinline__ float quantize_lane(float (&v)[WarpVec<D>::VPL], const float (&sg)[WarpVec<D>::VPL],
                                                const float (&tau)[(1 << BITS) - 1], int lane,
                                                int (&code)[WarpVec<D>::VPL]) {
   constexpr int VPL = WarpVec<D>::VPL;
-  constexpr int L = 1 << BITS;
   float ss = 0.0f;
 #pragma unroll
   for (int i = 0; i < VPL; ++i) {
@@ -79,10 +92,7 @@ __device__ __forceinline__ float quantize_lane(float (&v)[WarpVec<D>::VPL], cons
 #pragma unroll
   for (int i = 0; i < VPL; ++i) {
     const float w = n > 0.0f ? v[i] / n : 0.0f;  // = sqrt(D) * u
-    int q = 0;
-#pragma unroll
-    for (int k = 0; k < L - 1; ++k) q += (w >= tau[k]) ? 1 : 0;
-    code[i] = q;
+    code[i] = level_of<BITS>(w, tau);
   }
   return n;
 }
