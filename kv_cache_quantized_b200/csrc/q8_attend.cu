@@ -30,7 +30,7 @@ Q8Plan plan_decode(int64_t n_tok, int B, int G, int Hkv, int T, bool one, int ma
   pl.sp.chunk = 0;
   const int64_t shares = (pl.tl.tiles * Hkv * ((static_cast<int64_t>(T) + 31) / 32) + 1) / 2;
   pl.grid = static_cast<int>(shares < 1 ? 1 : shares < kSmCount ? shares : kSmCount);
-  pl.parts = static_cast<size_t>(pl.grid) * kQ8DecodeWarps * 2 * 8 * pl.nrg;
+  pl.parts = static_cast<size_t>(pl.grid) * q8_decode_warps(pl.nrg) * 2 * 8 * pl.nrg;
   return pl;
 }
 

@@ -65,7 +65,7 @@ struct Q8Tiles {
 
 // q8_decode.cu: tiles of up to 8 nrg query rows, one share of the key tiles a warp; any dtype.  The workspace holds two
 // partials of 8 nrg rows for each worker.
-constexpr int kQ8DecodeWarps = 12;
+constexpr int q8_decode_warps(int nrg) { return nrg == 1 ? 12 : 8; }  // a block
 axr_status q8_decode_launch(axr_dtype dtype, int d, bool i8, int nrg, int grid, const Q8Attend& a, const Q8Tiles& tl,
                             cudaStream_t st, const char* w);
 

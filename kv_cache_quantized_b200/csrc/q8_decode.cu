@@ -7,7 +7,7 @@ namespace {
 
 template <typename T, int D, bool I8, int NRG>
 axr_status launch(int grid, const Q8Attend& a, const Q8Tiles& tl, cudaStream_t st, const char* w) {
-  using P = DecodePlan<D>;
+  using P = DecodePlan<D, NRG>;
   auto k = q8_decode_kernel<T, D, I8, NRG>;
   axr_status rs = ensure_smem(k, P::bytes, w);
   if (rs != AXR_OK) return rs;

@@ -27,28 +27,23 @@
 #include <cuda.h>
 
 #include "dense_stream.cuh"
-#include "q8_attend.cuh"
+#include "q8_merge.cuh"
 
 namespace axr {
 
 constexpr int kDecTile = 32;      // tokens per tile
 constexpr int kDecMinTiles = 2;   // smallest share
 
-template <int D>
+// Twelve warps of 168 registers hold one row group without spilling, eight of 255 two; the rings fill shared memory.
+template <int D, int NRG>
 struct DecodePlan {
-  static constexpr int WARPS = kQ8DecodeWarps;
-  static constexpr int NS = 2;                              // stages per warp
+  static constexpr int WARPS = q8_decode_warps(NRG);
+  static constexpr int NS = NRG == 1 ? 2 : 3;               // stages per warp
   static constexpr size_t PLANE = kDecTile * D;             // the K (or V) codes of a stage
   static constexpr size_t STAGE = 2 * PLANE;
   static constexpr size_t OFF_MBAR = WARPS * NS * STAGE;
   static constexpr size_t bytes = 1024 + OFF_MBAR + WARPS * NS * 8;
 };
-
-__device__ __forceinline__ float q8_ex2(float x) {  // relative error 2^-22, as the planes'
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
 
 // 8-bit codes of two rows, 4 coordinates each, as 4 half2 (row a's coordinate, row b's coordinate)
 template <bool I8>
@@ -128,10 +123,10 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
 }
 
 template <typename T, int D, bool I8, int NRG>
-__global__ void __launch_bounds__(32 * kQ8DecodeWarps, 1)
+__global__ void __launch_bounds__(32 * q8_decode_warps(NRG), 1)
 q8_decode_kernel(const __grid_constant__ Q8Attend a, const __grid_constant__ Q8Tiles tl,
                  const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap) {
-  using P = DecodePlan<D>;
+  using P = DecodePlan<D, NRG>;
   constexpr int PL = sizeof(T) == 4 ? 2 : 1;  // fp16 planes of the queries and weights
   constexpr int KS = D / 16;       // k-steps of the score MMA, and 32-bit words of a lane's key run
   constexpr int NO = D / 16;       // coordinate tiles of the output
@@ -487,16 +482,12 @@ q8_decode_kernel(const __grid_constant__ Q8Attend a, const __grid_constant__ Q8T
   if (failed && lane == 0) atomicOr(a.status, 1u);
 }
 
-// Merge of the units cut by a share's edge, one block a (unit, row): weights 2^(m_s - max m), the unit's partials dealt
-// over the block's warps, their sums added in warp order.  Rows that a worker finished are left alone; rows of sequences
+// Merge of the units cut by a share's edge (q8_merge_row).  Rows that a worker finished are left alone; rows of sequences
 // without keys get zeros.  Launched as a programmatic dependent of the decode kernel.
-constexpr int kMergeWarps = 4;
 template <typename T, int D>
 __global__ void __launch_bounds__(32 * kMergeWarps)
 q8_decode_merge_kernel(const __grid_constant__ Q8Attend a, const __grid_constant__ Q8Tiles tl, int rows, int workers) {
-  constexpr int V = D / 32;
-  __shared__ float max_m[kMergeWarps], sum_l[kMergeWarps], sum_o[kMergeWarps][D];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
   const int per = tl.tpt * a.G, r = static_cast<int>(blockIdx.x) % per, unit = static_cast<int>(blockIdx.x) / per;
   const int hk = unit % a.Hkv;
   int b;
@@ -516,69 +507,8 @@ q8_decode_merge_kernel(const __grid_constant__ Q8Attend a, const __grid_constant
   // partial k of the unit: slot 0 of worker w0 + k, but slot 1 of w0 where the unit begins inside its share
   const int64_t first = (static_cast<int64_t>(w0) * 2 + (p0 > w0 * S ? 1 : 0)) * rows + r;
   const int64_t rest = static_cast<int64_t>(w0) * 2 * rows + r;
-  auto part = [&](int k) { return k == 0 ? first : rest + static_cast<int64_t>(k) * 2 * rows; };
-  // each warp its partials, U at a time: all loads of a group are in flight before its maximum is known
-  constexpr int U = 8;
-  float M = -INFINITY, L = 0.f, acc[V];
-#pragma unroll
-  for (int e = 0; e < V; ++e) acc[e] = 0.f;
-  for (int k0 = warp; k0 < n; k0 += U * kMergeWarps) {
-    float m[U], l[U], y[U][V];
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int k = k0 + u * kMergeWarps;
-      const bool on = k < n;
-      const int64_t pt = part(on ? k : k0);
-      m[u] = on ? __ldcg(a.ws_m + pt) : -INFINITY;
-      l[u] = on ? __ldcg(a.ws_l + pt) : 0.f;
-      const float* o = a.ws_o + pt * D + V * lane;
-      if constexpr (V == 4) {
-        const float4 q4 = __ldcg(reinterpret_cast<const float4*>(o));
-        y[u][0] = q4.x; y[u][1] = q4.y; y[u][2] = q4.z; y[u][3] = q4.w;
-      } else {
-        const float2 q2 = __ldcg(reinterpret_cast<const float2*>(o));
-        y[u][0] = q2.x; y[u][1] = q2.y;
-      }
-    }
-    float top = M;
-#pragma unroll
-    for (int u = 0; u < U; ++u) top = fmaxf(top, m[u]);   // drops a NaN, which comes back in the sums
-    const float back = top == -INFINITY ? 0.f : q8_ex2(M - top);
-    L *= back;
-#pragma unroll
-    for (int e = 0; e < V; ++e) acc[e] *= back;
-    M = top;
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const bool on = k0 + u * kMergeWarps < n;
-      const float f = !on || M == -INFINITY ? 0.f : q8_ex2(m[u] - M);
-      L = fmaf(f, l[u], L);
-#pragma unroll
-      for (int e = 0; e < V; ++e) acc[e] = fmaf(f, y[u][e], acc[e]);
-    }
-  }
-  if (lane == 0) {
-    max_m[warp] = M;
-    sum_l[warp] = L;
-  }
-#pragma unroll
-  for (int e = 0; e < V; ++e) sum_o[warp][V * lane + e] = acc[e];
-  __syncthreads();
-  const int j = threadIdx.x;
-  if (j >= D) return;
-  M = max_m[0];
-#pragma unroll
-  for (int w = 1; w < kMergeWarps; ++w) M = fmaxf(M, max_m[w]);
-  float x = 0.f;
-  L = 0.f;
-#pragma unroll
-  for (int w = 0; w < kMergeWarps; ++w) {
-    const float f = max_m[w] == -INFINITY ? 0.f : q8_ex2(max_m[w] - M);
-    L = fmaf(f, sum_l[w], L);
-    x = fmaf(f, sum_o[w][j], x);
-  }
   const int64_t orow = (sp.first + i0 + r / a.G) * a.Hq + static_cast<int64_t>(hk) * a.G + r % a.G;
-  static_cast<T*>(a.out)[orow * D + j] = from_float<T>(L == 0.f ? 0.f : x / L);
+  q8_merge_row<T, D, kMergeWarps>(a, n, [&](int k) { return k == 0 ? first : rest + static_cast<int64_t>(k) * 2 * rows; }, orow);
 }
 
 }  // namespace axr

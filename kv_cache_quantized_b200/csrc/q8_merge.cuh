@@ -1,36 +1,114 @@
-// Merge of q8_prefill_kernel's split partials.
+// Merge of the partials of attention over the 8-bit cache: weights 2^(m_k - max m).
 #pragma once
 
 #include "q8_attend.cuh"
 
 namespace axr {
 
-// Merge of the split partials of each live row of each (row tile, KV head): weights 2^(m_s - max m).  One block of D
-// threads a row.
-template <typename T, int D>
-__global__ void __launch_bounds__(D) q8_merge_kernel(const __grid_constant__ Q8Attend a, const Q8Tiles tl, int rows) {
-  const int64_t row = blockIdx.x;
-  const int j = threadIdx.x, r = static_cast<int>(row % rows), hk = static_cast<int>((row / rows) % a.Hkv);
+constexpr int kMergeWarps = 4;
+
+__device__ __forceinline__ float q8_ex2(float x) {  // relative error 2^-22, as the planes of the queries and weights
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// Merge of the n partials part(0) .. part(n - 1) of an output row by NW warps of a block: one, or all kMergeWarps, which
+// deal the partials among them and add their sums in warp order.  n = 0 gives zeros.
+template <typename T, int D, int NW, class Part>
+__device__ __forceinline__ void q8_merge_row(const Q8Attend& a, int n, Part part, int64_t orow) {
+  constexpr int V = D / 32;
+  __shared__ float max_m[kMergeWarps], sum_l[kMergeWarps], sum_o[kMergeWarps][D];
+  const int lane = threadIdx.x & 31, warp = NW == 1 ? 0 : threadIdx.x >> 5;
+  // each warp its partials, U at a time: all loads of a group are in flight before its maximum is known
+  constexpr int U = 8;
+  float M = -INFINITY, L = 0.f, acc[V];
+#pragma unroll
+  for (int e = 0; e < V; ++e) acc[e] = 0.f;
+  for (int k0 = warp; k0 < n; k0 += U * NW) {
+    float m[U], l[U], y[U][V];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int k = k0 + u * NW;
+      const bool on = k < n;
+      const int64_t pt = part(on ? k : k0);
+      m[u] = on ? __ldcg(a.ws_m + pt) : -INFINITY;
+      l[u] = on ? __ldcg(a.ws_l + pt) : 0.f;
+      const float* o = a.ws_o + pt * D + V * lane;
+      if constexpr (V == 4) {
+        const float4 q4 = __ldcg(reinterpret_cast<const float4*>(o));
+        y[u][0] = q4.x; y[u][1] = q4.y; y[u][2] = q4.z; y[u][3] = q4.w;
+      } else {
+        const float2 q2 = __ldcg(reinterpret_cast<const float2*>(o));
+        y[u][0] = q2.x; y[u][1] = q2.y;
+      }
+    }
+    float top = M;
+#pragma unroll
+    for (int u = 0; u < U; ++u) top = fmaxf(top, m[u]);   // drops a NaN, which comes back in the sums
+    const float back = top == -INFINITY ? 0.f : q8_ex2(M - top);
+    L *= back;
+#pragma unroll
+    for (int e = 0; e < V; ++e) acc[e] *= back;
+    M = top;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const bool on = k0 + u * NW < n;
+      const float f = !on || M == -INFINITY ? 0.f : q8_ex2(m[u] - M);
+      L = fmaf(f, l[u], L);
+#pragma unroll
+      for (int e = 0; e < V; ++e) acc[e] = fmaf(f, y[u][e], acc[e]);
+    }
+  }
+  if constexpr (NW == 1) {
+    T* dst = static_cast<T*>(a.out) + orow * D + V * lane;
+#pragma unroll
+    for (int e = 0; e < V; ++e) dst[e] = from_float<T>(L == 0.f ? 0.f : acc[e] / L);
+    return;
+  }
+  if (lane == 0) {
+    max_m[warp] = M;
+    sum_l[warp] = L;
+  }
+#pragma unroll
+  for (int e = 0; e < V; ++e) sum_o[warp][V * lane + e] = acc[e];
+  __syncthreads();
+  const int j = threadIdx.x;
+  if (j >= D) return;
+  M = max_m[0];
+#pragma unroll
+  for (int w = 1; w < kMergeWarps; ++w) M = fmaxf(M, max_m[w]);
+  float x = 0.f;
+  L = 0.f;
+#pragma unroll
+  for (int w = 0; w < kMergeWarps; ++w) {
+    const float f = max_m[w] == -INFINITY ? 0.f : q8_ex2(max_m[w] - M);
+    L = fmaf(f, sum_l[w], L);
+    x = fmaf(f, sum_o[w][j], x);
+  }
+  static_cast<T*>(a.out)[orow * D + j] = from_float<T>(L == 0.f ? 0.f : x / L);
+}
+
+// Merge of q8_prefill_kernel's split partials: one block a row of a (row tile, KV head), or, for up to 8 splits, a warp.
+// Launched as a programmatic dependent of it.
+template <typename T, int D, int NW>
+__global__ void __launch_bounds__(32 * kMergeWarps)
+q8_merge_kernel(const __grid_constant__ Q8Attend a, const __grid_constant__ Q8Tiles tl) {
+  const int64_t idx = NW == 1 ? static_cast<int64_t>(blockIdx.x) * kMergeWarps + (threadIdx.x >> 5) : blockIdx.x;
+  const int per = tl.tpt * a.G;
+  const int64_t unit = idx / per, tile = unit / a.Hkv;
+  const int r = static_cast<int>(idx - unit * per), hk = static_cast<int>(unit % a.Hkv);
+  if (tile >= tl.tiles) return;
   int b;
   int64_t i0;
-  q8_tile(a, tl, row / rows / a.Hkv, j & 31, b, i0);
+  q8_tile(a, tl, tile, threadIdx.x & 31, b, i0);
   const Q8Span sp = q8_span(a, b);
-  if (!q8_tile_live(a, tl, sp, i0, 1)) return;
+  if (!q8_tile_live(a, tl, sp, i0, threadIdx.x)) return;
   if (r >= min(tl.tpt, sp.count - static_cast<int>(i0)) * a.G) return;
-  const float* m = a.ws_m + row * a.splits;
-  const float* l = a.ws_l + row * a.splits;
-  const float* o = a.ws_o + row * a.splits * D + j;
-  float M = -INFINITY;
-  for (int s = 0; s < a.splits; ++s) M = fmaxf(M, m[s]);
-  float L = 0.f, acc = 0.f;
-  if (M != -INFINITY)
-    for (int s = 0; s < a.splits; ++s) {
-      const float w = exp2f(m[s] - M);
-      L = fmaf(w, l[s], L);
-      acc = fmaf(w, o[static_cast<size_t>(s) * D], acc);
-    }
+  asm volatile("griddepcontrol.wait;\n" ::: "memory");  // the partials are complete and visible after this
+  const int64_t p0 = (unit * kQ8PrefillRows + r) * a.splits;
   const int64_t orow = (sp.first + i0 + r / a.G) * a.Hq + static_cast<int64_t>(hk) * a.G + r % a.G;
-  static_cast<T*>(a.out)[orow * D + j] = from_float<T>(L > 0.f ? acc / L : 0.f);
+  q8_merge_row<T, D, NW>(a, a.splits, [&](int k) { return p0 + k; }, orow);
 }
 
 }  // namespace axr

@@ -12,9 +12,22 @@ axr_status launch(const Q8Attend& a, const Q8Tiles& tl, cudaStream_t st, const c
   const axr_status rs = ensure_smem(k, PrefillPlan<D>::bytes, w);
   if (rs != AXR_OK) return rs;
   k<<<static_cast<unsigned>(tl.tiles * a.Hkv * a.splits), kPfThreads, PrefillPlan<D>::bytes, st>>>(a, tl);
-  if (a.splits > 1)
-    q8_merge_kernel<T, D><<<static_cast<unsigned>(tl.tiles * a.Hkv * kQ8PrefillRows), D, 0, st>>>(a, tl,
-                                                                                                 kQ8PrefillRows);
+  if (a.splits > 1) {
+    auto merge = a.splits <= 8 ? q8_merge_kernel<T, D, 1> : q8_merge_kernel<T, D, kMergeWarps>;
+    // the merge keeps the attention kernel's split of L1: another one would have to wait for every SM to drain
+    cudaFuncSetAttribute(merge, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
+    const int64_t rows = tl.tiles * a.Hkv * tl.tpt * a.G;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(a.splits <= 8 ? (rows + kMergeWarps - 1) / kMergeWarps : rows));
+    cfg.blockDim = dim3(32 * kMergeWarps);
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    cudaLaunchKernelEx(&cfg, merge, a, tl);
+  }
   return check_launch(w);
 }
 

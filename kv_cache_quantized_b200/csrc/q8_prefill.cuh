@@ -163,6 +163,8 @@ q8_prefill_kernel(const __grid_constant__ Q8Attend a, const Q8Tiles tl) {
   const int n = end > begin ? (end - begin + kPfKeys - 1) / kPfKeys : 0;  // operand stages
   const int ns = end > begin ? (end - begin + kPfStep - 1) / kPfStep : 0;  // steps
 
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // a merge may get ready; it waits for this grid's end
+
   // ---- set-up: barriers, tensor memory, the query operand
   if (threadIdx.x == 0) {
 #pragma unroll
