@@ -384,7 +384,7 @@ AXR_API axr_status axr_pot_attend_decode(const float* q, const uint8_t* codes, c
  *   seq_lens     [dev] [B] int32, lengths with the new tokens: token i of sequence b has cache position
  *                seq_lens[b] - (cu[b + 1] - cu[b]) + (i - cu[b]);
  *   block_table  [dev] [B, max_blocks] int32, pool block of each logical block; block_tokens a power of two in
- *                [16, 2^20]; num_blocks the pools' block count;
+ *                [16, 2^20], max_blocks * block_tokens at most 2^30; num_blocks the pools' block count;
  *   cos_sin      [dev] [max_pos, rot] f32: row p holds the rot / 2 cosines, then the rot / 2 sines of position p's
  *                angles; rot a multiple of 16 up to d.  Pairs are (j, j + rot / 2), or (2 j, 2 j + 1) with interleaved
  *                != 0: (a, b) -> (a c - b s, b c + a s), each product and sum rounded to fp32 by itself; coordinates
@@ -401,7 +401,8 @@ AXR_API axr_status axr_pot_attend_decode(const float* q, const uint8_t* codes, c
  *   axr_attend_decode_paged.  q_out is fp32 whatever x_dtype, as the decode entry points take it.
  *
  * The 8-bit cache: codes [num_blocks, Hkv, bt, d] (kind AXR_Q8_INT: int8 in [-127, 127]; AXR_Q8_E4M3: e4m3 floats) and
- * one fp32 scale for each block of 16 tokens and KV head, [num_blocks, Hkv, bt / 16]; a coordinate is code * scale.
+ * one fp32 scale, not negative, for each block of 16 tokens and KV head, [num_blocks, Hkv, bt / 16]; a coordinate is
+ * code * scale.
  *
  * axr_q8_append_paged -- for each 16-token block and head that gets new tokens (keys after rotation):
  *     need = max |x| / 127 (int8), or the smallest power of two >= max |x| / 448 (e4m3); 0 when max |x| < 2^-100;
@@ -414,7 +415,9 @@ AXR_API axr_status axr_pot_attend_decode(const float* q, const uint8_t* codes, c
  *
  * axr_q8_attend_paged -- causal attention of the query tokens over the 8-bit cache that holds them already: token i of
  *   sequence b sees the cache positions up to its own.  out [n_tok, Hq, d] of x_dtype.  Sums and softmax statistics
- *   are fp32; queries and weights enter the tensor cores as hi and lo fp16 planes (about 22 bits).  A token that sees
+ *   are fp32, codes enter the tensor cores exactly.  Up to 16 query rows (tokens x heads of a group) a sequence, and all
+ *   fp32 calls: fp32 queries, and the weights of fp16 and fp32 calls, enter as hi and lo fp16 planes (about 22 bits).
+ *   More rows of 16-bit queries: one fp16 plane each (2^-11 a weight).  A token that sees
  *   nothing (seq_lens[b] smaller than its sequence's token count) gets 0.
  *   max_q an upper bound of a sequence's query tokens, or 0 if unknown; rows of a longer sequence are not written (and
  *   AXR_STATUS_BAD_INDEX is set).  T an upper bound of the lengths (longer ones are cut to it); seq_lens NULL: all T.

@@ -18,8 +18,10 @@ inline axr_status check_table(const char* w, const int32_t* table, int max_block
   *shift = block_shift_of(block_tokens);
   if (*shift < 0)
     return set_error(AXR_EINVAL, "%s: block_tokens=%d is not a power of two in [16, 2^20]", w, block_tokens);
-  if (max_blocks <= 0 || num_blocks <= 0 || static_cast<int64_t>(max_blocks) * block_tokens > 0x7fffffff)
+  if (max_blocks <= 0 || num_blocks <= 0)
     return set_error(AXR_EINVAL, "%s: bad sizes max_blocks=%d num_blocks=%d", w, max_blocks, num_blocks);
+  if (static_cast<int64_t>(max_blocks) * block_tokens > (1 << 30))  // token positions are 32-bit in the kernels
+    return set_error(AXR_EINVAL, "%s: max_blocks=%d x block_tokens=%d exceeds 2^30 tokens", w, max_blocks, block_tokens);
   if (!table) return set_error(AXR_EINVAL, "%s: null block table", w);
   if (!aligned(table, 4)) return set_error(AXR_EINVAL, "%s: misaligned block table", w);
   return AXR_OK;

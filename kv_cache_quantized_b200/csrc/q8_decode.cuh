@@ -15,8 +15,9 @@
 // is empty for 8 rows:
 //   S^T = K Q^T    A = 16 tokens x 16 coordinates of codes, B = the queries;
 //   O^T += V^T P^T A = 16 coordinates x 16 tokens of codes, B = the weights, transposed in registers (movmatrix).
-// The codes enter exactly; queries and softmax weights as PL fp16 planes: hi and lo for fp32 (about 22 bits), one for
-// 16-bit queries and outputs (which a power of two makes exact; the weights round to 2^-11).  Coordinates and tokens may
+// The codes enter exactly; queries as PQ fp16 planes, hi and lo (about 22 bits) for fp32, one for 16-bit types, which a
+// power of two makes exact; softmax weights as PP planes, one for bf16 (a rounding to 2^-11, where the output's is 2^-9),
+// hi and lo for fp16 and fp32.  Coordinates and tokens may
 // be summed in any order, so each lane reads 16-byte runs of a code row: of the key rows 8 n + g the bytes
 // [D/4 t, D/4 t + D/4), whose word s feeds k-step s; of the value rows 2 t, 2 t + 1, 2 t + 8, 2 t + 9 (+ 16) the bytes
 // [D/8 g, D/8 g + D/8), bytes 2 j and 2 j + 1 going to rows g and g + 8 of coordinate tile j.  Every code is read from
@@ -25,6 +26,8 @@
 #pragma once
 
 #include <cuda.h>
+
+#include <type_traits>
 
 #include "dense_stream.cuh"
 #include "q8_merge.cuh"
@@ -127,7 +130,8 @@ __global__ void __launch_bounds__(32 * q8_decode_warps(NRG), 1)
 q8_decode_kernel(const __grid_constant__ Q8Attend a, const __grid_constant__ Q8Tiles tl,
                  const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap) {
   using P = DecodePlan<D, NRG>;
-  constexpr int PL = sizeof(T) == 4 ? 2 : 1;  // fp16 planes of the queries and weights
+  constexpr int PQ = sizeof(T) == 4 ? 2 : 1;                                // fp16 planes of the queries
+  constexpr int PP = std::is_same<T, __nv_bfloat16>::value ? 1 : 2;         // and of the weights
   constexpr int KS = D / 16;       // k-steps of the score MMA, and 32-bit words of a lane's key run
   constexpr int NO = D / 16;       // coordinate tiles of the output
   constexpr int VB = D / 8;        // bytes of a lane's value run, and its output coordinates
@@ -215,7 +219,7 @@ q8_decode_kernel(const __grid_constant__ Q8Attend a, const __grid_constant__ Q8T
     scales_of(r0, r1, sc);
 
     // the query operand of this lane: row 8 n + g of group n, coordinates [D/4 t, D/4 t + D/4)
-    uint32_t qf[NRG][PL][KS][2];
+    uint32_t qf[NRG][PQ][KS][2];
     float f_row[NRG][2];
     int lim[NRG][2];               // rows 8 n + 2 t + {0, 1}, whose scores and output this lane holds: keys < lim are visible
 #pragma unroll
@@ -250,7 +254,7 @@ q8_decode_kernel(const __grid_constant__ Q8Attend a, const __grid_constant__ Q8T
       for (int s = 0; s < KS; ++s)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          if constexpr (PL == 2) split_h2(v[s][2 * e] * up, v[s][2 * e + 1] * up, qf[n][0][s][e], qf[n][1][s][e]);
+          if constexpr (PQ == 2) split_h2(v[s][2 * e] * up, v[s][2 * e + 1] * up, qf[n][0][s][e], qf[n][PQ - 1][s][e]);
           else qf[n][0][s][e] = pack_h2(v[s][2 * e] * up, v[s][2 * e + 1] * up);
         }
 #pragma unroll
@@ -320,7 +324,7 @@ q8_decode_kernel(const __grid_constant__ Q8Attend a, const __grid_constant__ Q8T
 #pragma unroll
             for (int n = 0; n < NRG; ++n)
 #pragma unroll
-              for (int p = 0; p < PL; ++p)
+              for (int p = 0; p < PQ; ++p)
                 mma16816(sc4[n][h], a0, a1, a2, a3, qf[n][p][4 * c + e][0], qf[n][p][4 * c + e][1]);
           }
         }
@@ -341,7 +345,7 @@ q8_decode_kernel(const __grid_constant__ Q8Attend a, const __grid_constant__ Q8T
       const float vi = vref > 0.f ? 16384.f / vref : 0.f;
       const float vf[2] = {vs[0] * vi, vs[1] * vi};
 
-      uint32_t pf[NRG][PL][2][2];
+      uint32_t pf[NRG][PP][2][2];
 #pragma unroll
       for (int n = 0; n < NRG; ++n) {
         float p[2][4], mx[2] = {-INFINITY, -INFINITY}, m_use[2], alpha[2];  // [row][16 h + g, + 8]
@@ -385,11 +389,11 @@ q8_decode_kernel(const __grid_constant__ Q8Attend a, const __grid_constant__ Q8T
           }
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          if constexpr (PL == 2) {
+          if constexpr (PP == 2) {
             uint32_t hi, lo;
             split_h2(p[0][e], p[1][e], hi, lo);
             pf[n][0][e >> 1][e & 1] = transpose8x8(hi);
-            pf[n][PL - 1][e >> 1][e & 1] = transpose8x8(lo);
+            pf[n][PP - 1][e >> 1][e & 1] = transpose8x8(lo);
           } else {
             pf[n][0][e >> 1][e & 1] = transpose8x8(pack_h2(p[0][e], p[1][e]));
           }
@@ -422,7 +426,7 @@ q8_decode_kernel(const __grid_constant__ Q8Attend a, const __grid_constant__ Q8T
 #pragma unroll
           for (int n = 0; n < NRG; ++n)
 #pragma unroll
-            for (int p = 0; p < PL; ++p)
+            for (int p = 0; p < PP; ++p)
 #pragma unroll
               for (int j = 0; j < 2; ++j)
                 mma16816(o[n][2 * e + j], b0[2 * j], b0[2 * j + 1], b1[2 * j], b1[2 * j + 1], pf[n][p][h][0],
@@ -494,15 +498,17 @@ q8_decode_merge_kernel(const __grid_constant__ Q8Attend a, const __grid_constant
   int64_t i0;
   q8_tile(a, tl, unit / a.Hkv, lane, b, i0);
   const Q8Span sp = q8_span(a, b);
-  if (!q8_tile_live(a, tl, sp, i0, threadIdx.x)) return;
-  if (r >= min(tl.tpt, sp.count - static_cast<int>(i0)) * a.G) return;
+  // every block waits, those without a row too: this grid's end stands for the attention kernel's
+  const auto wait = [] { asm volatile("griddepcontrol.wait;\n" ::: "memory"); };
+  if (!q8_tile_live(a, tl, sp, i0, threadIdx.x)) return wait();
+  if (r >= min(tl.tpt, sp.count - static_cast<int>(i0)) * a.G) return wait();
   int64_t seq0, total;
   q8_flat(a, tl, lane, -1, b, seq0, total);
   const int64_t S = q8_share(total, workers);
   const Q8Extent ext = q8_extent(a, tl, b);
   const int64_t p0 = seq0 + (q8_div(i0, tl.tpt) * a.Hkv + hk) * ext.tiles, p1 = p0 + ext.tiles;  // the unit's flat tiles
   const int w0 = static_cast<int>(q8_div(p0, S)), n = p1 > p0 ? static_cast<int>(q8_div(p1 - 1, S)) - w0 + 1 : 0;
-  asm volatile("griddepcontrol.wait;\n" ::: "memory");  // the partials are complete and visible after this
+  wait();                                                 // the partials are complete and visible after this
   if (n == 1) return;                                     // one worker finished it
   // partial k of the unit: slot 0 of worker w0 + k, but slot 1 of w0 where the unit begins inside its share
   const int64_t first = (static_cast<int64_t>(w0) * 2 + (p0 > w0 * S ? 1 : 0)) * rows + r;

@@ -98,14 +98,16 @@ q8_merge_kernel(const __grid_constant__ Q8Attend a, const __grid_constant__ Q8Ti
   const int per = tl.tpt * a.G;
   const int64_t unit = idx / per, tile = unit / a.Hkv;
   const int r = static_cast<int>(idx - unit * per), hk = static_cast<int>(unit % a.Hkv);
-  if (tile >= tl.tiles) return;
+  // every block waits, those without a row too: this grid's end stands for the attention kernel's
+  const auto wait = [] { asm volatile("griddepcontrol.wait;\n" ::: "memory"); };
+  if (tile >= tl.tiles) return wait();
   int b;
   int64_t i0;
   q8_tile(a, tl, tile, threadIdx.x & 31, b, i0);
   const Q8Span sp = q8_span(a, b);
-  if (!q8_tile_live(a, tl, sp, i0, threadIdx.x)) return;
-  if (r >= min(tl.tpt, sp.count - static_cast<int>(i0)) * a.G) return;
-  asm volatile("griddepcontrol.wait;\n" ::: "memory");  // the partials are complete and visible after this
+  if (!q8_tile_live(a, tl, sp, i0, threadIdx.x)) return wait();
+  if (r >= min(tl.tpt, sp.count - static_cast<int>(i0)) * a.G) return wait();
+  wait();  // the partials are complete and visible after this
   const int64_t p0 = (unit * kQ8PrefillRows + r) * a.splits;
   const int64_t orow = (sp.first + i0 + r / a.G) * a.Hq + static_cast<int64_t>(hk) * a.G + r % a.G;
   q8_merge_row<T, D, NW>(a, a.splits, [&](int k) { return p0 + k; }, orow);

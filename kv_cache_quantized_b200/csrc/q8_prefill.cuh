@@ -41,7 +41,7 @@ struct PrefillPlan {
   static constexpr uint32_t OFF_SC = 6 * TILE;             // [4][32] floats: a key tile's ks[8], off[8], winv[8], lref
   static constexpr uint32_t OFF_BL = OFF_SC + 4 * 32 * 4;  // [4][8] ints: scale blocks of a tile, by converter warp
   static constexpr uint32_t OFF_BAR = OFF_BL + 4 * 8 * 4;
-  static constexpr size_t bytes = 1024 + OFF_BAR + 22 * 8;
+  static constexpr size_t bytes = 1024 + OFF_BAR + 26 * 8;
   static constexpr uint32_t COLS = 512, COL_S = 0, COL_O = 256;  // tensor memory: S of the row tiles, then O, 128 each
   static constexpr int CH = D / 16;                        // 16-byte code chunks of a row
   static constexpr int NL = kPfKeys * CH / 128;            // chunks a converter thread holds of a tile
@@ -142,7 +142,8 @@ q8_prefill_kernel(const __grid_constant__ Q8Attend a, const Q8Tiles tl) {
   // by stage: operands written, operands read; by row tile and S buffer: S written, weights written, output updated
   uint64_t *k_full = bar, *v_full = bar + 2, *k_free = bar + 4, *v_free = bar + 6;
   uint64_t *s_full = bar + 8, *p_full = bar + 12, *pv_done = bar + 16;  // [row tile][S buffer]
-  uint32_t* tm_slot = reinterpret_cast<uint32_t*>(bar + 20);
+  uint64_t* drain = bar + 20;                                            // [issuing warp], when a wait gave up
+  uint32_t* tm_slot = reinterpret_cast<uint32_t*>(bar + 24);
   uint32_t* failed = tm_slot + 1;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
@@ -179,6 +180,7 @@ q8_prefill_kernel(const __grid_constant__ Q8Attend a, const Q8Tiles tl) {
       tc::mbar_init(s_full + i, 1);
       tc::mbar_init(p_full + i, 128);
       tc::mbar_init(pv_done + i, 1);
+      tc::mbar_init(drain + i, 1);
     }
     *failed = 0;
   }
@@ -379,7 +381,13 @@ q8_prefill_kernel(const __grid_constant__ Q8Attend a, const Q8Tiles tl) {
         __syncwarp();
       }
     }
-    if (!ok) *failed = 1;
+    if (!ok) {
+      // a wait gave up: let the products issued so far end, bounded again, before tensor memory is freed
+      *failed = 1;
+      if (elect_one()) mma_commit(drain + (warp - 12));
+      __syncwarp();
+      warp_wait(drain + (warp - 12), 0);
+    }
   } else {
     if (warp < 4 * nq) {
     // ---- softmax: thread = row

@@ -487,3 +487,127 @@ def test_refusals():
     cu = torch.zeros(3, dtype=torch.int32, device="cuda")
     ops.q8_append_paged(none, none, *dev, tab, tl, cu_new=cu)
     assert ops.q8_attend_paged(torch.zeros((0, 8, 128), device="cuda"), *dev, tab, tl, cu_q=cu).shape == (0, 8, 128)
+
+
+# ---- further shapes of a call ----------------------------------------------------------------------------------------
+
+def test_batches_of_more_than_32_sequences():
+    """Sequence lookups of several rounds: 75 sequences, empty ones among them, through every entry point."""
+    rng = np.random.default_rng(8)
+    counts = rng.integers(0, 4, 75).tolist()
+    lens = [c + int(x) for c, x in zip(counts, rng.integers(0, 60, 75))]
+    lens[40] = counts[40] = 0
+    d, Hq, Hkv, bt, kind = 64, 4, 2, 16, "i8"
+    bt_ = Batch(counts, lens, Hq, Hkv, d, bt, "f16", 41)
+    tab, pools = rope_table(200, d), filled(bt_, kind)
+    dev = [cuda(p) for p in pools]
+    qr = ops.q8_append_paged(bt_.k, bt_.v, *dev, bt_.t["table"], bt_.t["lens"], kind=kind, cu_new=bt_.t["cu"], q=bt_.q,
+                             cos_sin=cuda(tab))
+    q8.append(bt_.rotated(bt_.kn, tab, False), pools[0], pools[1], bt_.table, lens, counts, bt, kind)
+    q8.append([bt_.rows(bt_.vn, b) for b in range(75)], pools[2], pools[3], bt_.table, lens, counts, bt, kind)
+    assert same(dev, [cuda(p) for p in pools])
+    qn = qr.float().cpu().numpy()
+    for dtype, max_q in (("f16", 3), ("f16", None), ("f32", None)):  # one tile a sequence, tcgen05, flat tiles
+        qq = qr.to(DT[dtype])
+        out = ops.q8_attend_paged(qq, *dev, bt_.t["table"], bt_.t["lens"], kind=kind, cu_q=bt_.t["cu"], max_q=max_q)
+        check_attention(out, bt_, [qn[bt_.cu[b]:bt_.cu[b + 1]] for b in range(75)], pools, kind, 1 / math.sqrt(d), dtype)
+    one = Batch([1] * 75, [max(x, 1) for x in lens], Hq, Hkv, d, bt, "bf16", 42, pad=0)
+    pools = filled(one, kind)
+    out = ops.q8_attend_paged(one.q, *[cuda(p) for p in pools], one.t["table"], one.t["lens"], kind=kind)
+    check_attention(out, one, [one.rows(one.qn, b) for b in range(75)], pools, kind, 1 / math.sqrt(d), "bf16")
+
+
+@pytest.mark.parametrize("dtype,counts,max_q", [("bf16", [1], 1), ("f32", [1], 1), ("f16", [9], 9), ("f16", [40], None),
+                                                ("bf16", [300], None), ("f32", [3], None)])
+def test_long_axes_split_over_the_gpu(dtype, counts, max_q):
+    """One sequence of 20,011 tokens: the axis is cut into many partials, merged."""
+    d, Hq, Hkv, bt, kind = 128, 4, 1, 64, "e4m3"
+    bt_ = Batch(counts, [20011], Hq, Hkv, d, bt, dtype, 43, pad=2)
+    pools = filled(bt_, kind)
+    out = torch.full((bt_.n_tok, Hq, d), -3.0, dtype=DT[dtype], device="cuda")
+    ops.q8_attend_paged(bt_.q, *[cuda(p) for p in pools], bt_.t["table"], bt_.t["lens"], kind=kind, cu_q=bt_.t["cu"],
+                        max_q=max_q, out=out)
+    check_attention(out, bt_, [bt_.rows(bt_.qn, 0)], pools, kind, 1 / math.sqrt(d), dtype, out_fill=-3.0)
+
+
+@pytest.mark.parametrize("scale", [-0.05, 0.0])
+@pytest.mark.parametrize("counts", [[1, 1], [40, 90]])
+def test_scales_that_are_not_positive(scale, counts):
+    bt_ = Batch(counts, [100, 300], 8, 2, 128, 32, "bf16", 44, pad=0)
+    pools = filled(bt_, "i8")
+    out = ops.q8_attend_paged(bt_.q, *[cuda(p) for p in pools], bt_.t["table"], bt_.t["lens"], cu_q=bt_.t["cu"], scale=scale)
+    check_attention(out, bt_, [bt_.rows(bt_.qn, b) for b in range(2)], pools, "i8", scale, "bf16")
+
+
+@pytest.mark.parametrize("counts", [[1, 1, 1], [30, 80, 64]])
+def test_blocks_of_zero_values_keep_their_weight(counts):
+    """Values that are zero for a stretch of tokens (scale 0), tiny or large elsewhere: the zeros count in the
+    normaliser."""
+    bt_ = Batch(counts, [200, 130, 64], 8, 2, 128, 32, "f16", 45, pad=0)
+    kc, ks, vc, vs = filled(bt_, "i8")
+    for b in range(3):
+        for t in range(0, 64, 16):
+            page = bt_.table[b, t // 32]
+            vc[page, :, t % 32:t % 32 + 16], vs[page, :, t % 32 // 16] = 0, 0.0
+        for t in range(64, bt_.lens[b] - 48, 16):
+            vs[bt_.table[b, t // 32], :, t % 32 // 16] *= np.float32(2.0 ** -9)
+    pools = [kc, ks, vc, vs]
+    out = ops.q8_attend_paged(bt_.q, *[cuda(p) for p in pools], bt_.t["table"], bt_.t["lens"], cu_q=bt_.t["cu"])
+    check_attention(out, bt_, [bt_.rows(bt_.qn, b) for b in range(3)], pools, "i8", 1 / math.sqrt(128), "f16")
+
+
+def test_pools_of_more_than_four_gigabytes():
+    """Rows of the last pool blocks: element offsets pass 32 bits (K and V pools of 4.3 GB each)."""
+    d, Hq, Hkv, bt, kind = 128, 8, 2, 64, "i8"
+    nb = (1 << 32) // (Hkv * bt * d) + 40
+    lens, counts = [200, 77, 130], [40, 1, 130]
+    bt_ = Batch(counts, lens, Hq, Hkv, d, bt, "bf16", 46, pad=0)
+    small = filled(bt_, kind)
+    off = nb - bt_.nb
+    big = [torch.empty((nb,) + p.shape[1:], dtype=torch.uint8 if p.dtype == np.uint8 else torch.float32, device="cuda")
+           for p in small]
+    for a, p in zip(big, small):
+        a[off:] = cuda(p)
+    table = cuda(np.where(bt_.table >= 0, bt_.table + off, -7).astype(np.int32))
+    near = [cuda(p) for p in small]
+    tab = cuda(rope_table(300, d))
+    for tb, pl in ((table, big), (bt_.t["table"], near)):
+        qr = ops.q8_append_paged(bt_.k, bt_.v, *pl, tb, bt_.t["lens"], kind=kind, cu_new=bt_.t["cu"], q=bt_.q, cos_sin=tab)
+    assert same([a[off:].contiguous() for a in big], near)
+    last = torch.from_numpy(bt_.cu[1:].astype(np.int64) - 1).cuda()
+    for q, kw in ((qr, dict(cu_q=bt_.t["cu"])), (qr[last].contiguous(), {})):
+        assert torch.equal(ops.q8_attend_paged(q, *big, table, bt_.t["lens"], kind=kind, T=256, **kw),
+                           ops.q8_attend_paged(q, *near, bt_.t["table"], bt_.t["lens"], kind=kind, T=256, **kw))
+    del big
+    torch.cuda.empty_cache()
+
+
+def test_two_graphs_that_share_a_workspace():
+    """A decode step and a chunk, each captured with one caller workspace, replayed in turn."""
+    d, Hq, Hkv, bt = 128, 8, 2, 32
+    a = Batch([1] * 3, [900, 17, 640], Hq, Hkv, d, bt, "bf16", 47, pad=0)
+    b = Batch([33, 70], [900, 300], Hq, Hkv, d, bt, "bf16", 48, pad=0)
+    pa, pb = [cuda(p) for p in filled(a, "i8")], [cuda(p) for p in filled(b, "i8")]
+    need = max(ops.q8_attend_workspace_bytes(3, 1, 3, Hq, Hkv, 960, d),
+               ops.q8_attend_workspace_bytes(103, 70, 2, Hq, Hkv, 960, d))
+    ws = torch.empty(need, dtype=torch.uint8, device="cuda")
+    calls = [lambda o=None: ops.q8_attend_paged(a.q, *pa, a.t["table"], a.t["lens"], T=960, workspace=ws, out=o),
+             lambda o=None: ops.q8_attend_paged(b.q, *pb, b.t["table"], b.t["lens"], cu_q=b.t["cu"], max_q=70, T=960,
+                                                workspace=ws, out=o)]
+    want = [c() for c in calls]
+    outs = [torch.zeros_like(w) for w in want]
+    graphs = []
+    for c, o in zip(calls, outs):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            c(o)
+        graphs.append(g)
+    for _ in range(2):
+        for o in outs:
+            o.zero_()
+        for g in graphs:
+            g.replay()
+        assert all(torch.equal(o, w) for o, w in zip(outs, want))
+    with pytest.raises(_abi.AxrError) as e:
+        ops.q8_attend_paged(a.q, *pa, a.t["table"], a.t["lens"], T=960, workspace=ws[:64])
+    assert e.value.status == 4

@@ -100,7 +100,7 @@ def test_q8_append_argument_errors(L):
     assert _append8(L, bt=48) == 1 and _append8(L, bt=8) == 1 and _append8(L, nb=0) == 1 and _append8(L, tab=None) == 1
     assert _append8(L, ks=255) == 1 and _append8(L, ks=257) == 1 and _append8(L, k=FAKE + 2) == 1
     assert _append8(L, ks=128) == 1 and _append8(L, kc=None) == 1 and _append8(L, kc=FAKE + 4) == 1
-    assert _append8(L, lens=None) == 1 and _append8(L, mp=0) == 1 and _append8(L, mb=1 << 27) == 1
+    assert _append8(L, lens=None) == 1 and _append8(L, mp=0) == 1 and _append8(L, mb=(1 << 25) + 1) == 1
     assert _append8(L, n=0, B=0) == 0
 
 
