@@ -73,45 +73,109 @@ struct Q8Extent {
   int rts;    // row tiles
   int tiles;  // key tiles of each (those of its last row tile)
 };
-__device__ __forceinline__ Q8Extent q8_extent(const Q8Attend& a, const Q8Tiles& tl, int b) {
-  const Q8Span sp = q8_span(a, b);
+__device__ __forceinline__ Q8Extent q8_extent(const Q8Tiles& tl, const Q8Span& sp) {
   Q8Extent e;
   e.rts = tl.one ? (sp.count > 0 && sp.count <= tl.tpt ? 1 : 0) : (sp.count + tl.tpt - 1) / tl.tpt;
   e.tiles = e.rts > 0 ? (sp.len + kDecTile - 1) / kDecTile : 0;
   return e;
 }
 
-// The flat tile sequence: where sequence b's tiles begin (begin), and how many there are in all (total).  One warp.
-// find >= 0: b is instead the sequence that holds flat tile `find`.
-__device__ __forceinline__ void q8_flat(const Q8Attend& a, const Q8Tiles& tl, int lane, int64_t find, int& b,
-                                        int64_t& begin, int64_t& total) {
-  int64_t sum = 0, at = 0;
-  int hit = b;
-  for (int b0 = 0; b0 < a.B; b0 += 32) {
-    int64_t n = 0;
-    if (b0 + lane < a.B) {
-      const Q8Extent e = q8_extent(a, tl, b0 + lane);
-      n = static_cast<int64_t>(e.rts) * a.Hkv * e.tiles;
-    }
+// A sequence in the flat tile sequence.
+struct Q8Place {
+  int b;
+  int64_t begin;  // its first tile
+  Q8Span sp;
+  Q8Extent ext;
+};
+
+// The flat tile sequence as a warp holds it: lane l has sequences l and 32 + l (their entries read once, in one round
+// trip); batches of more than 64 sequences are read again by each search.
+struct Q8Flat {
+  Q8Span sp[2];
+  Q8Extent ext[2];
+  int64_t ex[2], n[2];  // tiles before, tiles of
+  int64_t total;
+
+  __device__ __forceinline__ static void scan(const Q8Attend& a, const Q8Tiles& tl, int lane, int b0, int64_t& sum,
+                                              Q8Span& sp, Q8Extent& e, int64_t& ex, int64_t& n) {
+    const bool on = b0 + lane < a.B;
+    sp = q8_span(a, on ? b0 + lane : 0);
+    e = q8_extent(tl, sp);
+    n = on ? static_cast<int64_t>(e.rts) * a.Hkv * e.tiles : 0;
     int64_t inc = n;
 #pragma unroll
     for (int m = 1; m < 32; m <<= 1) {
       const int64_t o = __shfl_up_sync(0xffffffffu, inc, m);
       if (lane >= m) inc += o;
     }
-    const int64_t ex = sum + inc - n;  // tiles before this lane's sequence
-    const bool mine = find >= 0 ? n > 0 && ex <= find && find < ex + n : b0 + lane == b;
-    const unsigned who = __ballot_sync(0xffffffffu, mine);
-    if (who) {
-      hit = b0 + __ffs(who) - 1;
-      at = __shfl_sync(0xffffffffu, ex, __ffs(who) - 1);
-    }
+    ex = sum + inc - n;
     sum += __shfl_sync(0xffffffffu, inc, 31);
   }
-  b = hit;
-  begin = at;
-  total = sum;
-}
+
+  __device__ __forceinline__ void load(const Q8Attend& a, const Q8Tiles& tl, int lane) {
+    total = 0;
+    scan(a, tl, lane, 0, total, sp[0], ext[0], ex[0], n[0]);
+    n[1] = 0;
+    if (a.B > 32) scan(a, tl, lane, 32, total, sp[1], ext[1], ex[1], n[1]);
+    for (int b0 = 64; b0 < a.B; b0 += 32) {
+      Q8Span s;
+      Q8Extent e;
+      int64_t x, y;
+      scan(a, tl, lane, b0, total, s, e, x, y);
+    }
+  }
+
+  __device__ __forceinline__ static void take(Q8Place& r, const Q8Span& sp, const Q8Extent& e, int64_t ex, int b0,
+                                              int src) {
+    r.b = b0 + src;
+    r.begin = __shfl_sync(0xffffffffu, ex, src);
+    r.sp.first = __shfl_sync(0xffffffffu, sp.first, src);
+    r.sp.count = __shfl_sync(0xffffffffu, sp.count, src);
+    r.sp.pos0 = __shfl_sync(0xffffffffu, sp.pos0, src);
+    r.sp.len = __shfl_sync(0xffffffffu, sp.len, src);
+    r.ext.rts = __shfl_sync(0xffffffffu, e.rts, src);
+    r.ext.tiles = __shfl_sync(0xffffffffu, e.tiles, src);
+  }
+
+  // The first sequence for which pick(b, tiles before, tiles of) holds; x < total and b < B always have one.
+  template <class Pick>
+  __device__ __forceinline__ Q8Place find(const Q8Attend& a, const Q8Tiles& tl, int lane, Pick pick) const {
+    Q8Place r;
+    unsigned who = __ballot_sync(0xffffffffu, pick(lane, ex[0], n[0]));
+    if (who) {
+      take(r, sp[0], ext[0], ex[0], 0, __ffs(who) - 1);
+      return r;
+    }
+    who = __ballot_sync(0xffffffffu, a.B > 32 && pick(32 + lane, ex[1], n[1]));
+    if (who) {
+      take(r, sp[1], ext[1], ex[1], 32, __ffs(who) - 1);
+      return r;
+    }
+    int64_t sum = __shfl_sync(0xffffffffu, ex[1] + n[1], 31);  // tiles of the first 64
+    for (int b0 = 64; b0 < a.B; b0 += 32) {
+      Q8Span s;
+      Q8Extent e;
+      int64_t x, y;
+      scan(a, tl, lane, b0, sum, s, e, x, y);
+      who = __ballot_sync(0xffffffffu, pick(b0 + lane, x, y));
+      if (who) {
+        take(r, s, e, x, b0, __ffs(who) - 1);
+        return r;
+      }
+    }
+    r.b = 0;
+    r.begin = 0;
+    r.sp = {0, 0, 0, 0};
+    r.ext = {0, 1};
+    return r;
+  }
+  __device__ __forceinline__ Q8Place at_tile(const Q8Attend& a, const Q8Tiles& tl, int lane, int64_t x) const {
+    return find(a, tl, lane, [=](int, int64_t ex_, int64_t n_) { return ex_ <= x && x < ex_ + n_; });
+  }
+  __device__ __forceinline__ Q8Place of(const Q8Attend& a, const Q8Tiles& tl, int lane, int b) const {
+    return find(a, tl, lane, [=](int c, int64_t, int64_t) { return c == b; });
+  }
+};
 
 __device__ __forceinline__ int64_t q8_share(int64_t total, int workers) {
   const int64_t s = q8_div(total + workers - 1, workers);
@@ -150,19 +214,20 @@ q8_decode_kernel(const __grid_constant__ Q8Attend a, const __grid_constant__ Q8T
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the merge may get ready; it waits for this grid's end
   const int workers = gridDim.x * P::WARPS;
   const int worker = blockIdx.x + gridDim.x * warp;
-  int b = 0;
-  int64_t seq0 = 0, total = 0;
-  q8_flat(a, tl, lane, 0, b, seq0, total);
-  const int64_t S = q8_share(total, workers);
-  const int64_t x0 = worker * S, x1 = min(x0 + S, total);
+  Q8Flat flat;
+  flat.load(a, tl, lane);
+  const int64_t S = q8_share(flat.total, workers);
+  const int64_t x0 = worker * S, x1 = min(x0 + S, flat.total);
   const bool wide = a.shift >= 5;  // a 32-token tile lies in one pool block
   uint32_t seq = 0;                // tiles consumed: stage seq % NS, phase parity (seq / NS) & 1
   bool failed = false;
 
   for (int64_t x = x0; x < x1;) {
-    q8_flat(a, tl, lane, x, b, seq0, total);
-    const Q8Extent ext = q8_extent(a, tl, b);
-    const Q8Span sp = q8_span(a, b);
+    const Q8Place at = flat.at_tile(a, tl, lane, x);
+    const int b = at.b;
+    const int64_t seq0 = at.begin;
+    const Q8Extent ext = at.ext;
+    const Q8Span sp = at.sp;
     const int u = static_cast<int>(q8_div(x - seq0, ext.tiles));  // unit in the sequence: row tile, then KV head
     const int k0 = static_cast<int>(x - seq0 - static_cast<int64_t>(u) * ext.tiles);  // first key tile
     const int k1 = static_cast<int>(min(static_cast<int64_t>(ext.tiles), k0 + (x1 - x)));
@@ -497,16 +562,17 @@ q8_decode_merge_kernel(const __grid_constant__ Q8Attend a, const __grid_constant
   int b;
   int64_t i0;
   q8_tile(a, tl, unit / a.Hkv, lane, b, i0);
-  const Q8Span sp = q8_span(a, b);
+  Q8Flat flat;
+  flat.load(a, tl, lane);
+  const Q8Place at = flat.of(a, tl, lane, b);
+  const Q8Span sp = at.sp;
   // every block waits, those without a row too: this grid's end stands for the attention kernel's
   const auto wait = [] { asm volatile("griddepcontrol.wait;\n" ::: "memory"); };
   if (!q8_tile_live(a, tl, sp, i0, threadIdx.x)) return wait();
   if (r >= min(tl.tpt, sp.count - static_cast<int>(i0)) * a.G) return wait();
-  int64_t seq0, total;
-  q8_flat(a, tl, lane, -1, b, seq0, total);
-  const int64_t S = q8_share(total, workers);
-  const Q8Extent ext = q8_extent(a, tl, b);
-  const int64_t p0 = seq0 + (q8_div(i0, tl.tpt) * a.Hkv + hk) * ext.tiles, p1 = p0 + ext.tiles;  // the unit's flat tiles
+  const int64_t S = q8_share(flat.total, workers);
+  const Q8Extent ext = at.ext;
+  const int64_t p0 = at.begin + (q8_div(i0, tl.tpt) * a.Hkv + hk) * ext.tiles, p1 = p0 + ext.tiles;  // the unit's flat tiles
   const int w0 = static_cast<int>(q8_div(p0, S)), n = p1 > p0 ? static_cast<int>(q8_div(p1 - 1, S)) - w0 + 1 : 0;
   wait();                                                 // the partials are complete and visible after this
   if (n == 1) return;                                     // one worker finished it
