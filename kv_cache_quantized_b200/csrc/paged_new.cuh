@@ -94,6 +94,15 @@ __device__ __forceinline__ int64_t page_row(const PagedNew& p, int b, int pos, i
   return (static_cast<int64_t>(page) * Hkv) << p.shift;
 }
 
+// Packed fp32 product, each half rounded to nearest.
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  unsigned long long rd;
+  asm("mul.rn.f32x2 %0, %1, %2;"
+      : "=l"(rd)
+      : "l"(*reinterpret_cast<unsigned long long*>(&a)), "l"(*reinterpret_cast<unsigned long long*>(&b)));
+  return *reinterpret_cast<float2*>(&rd);
+}
+
 // ---- rows of 8 coordinates a lane --------------------------------------------------------------------------------
 
 __device__ __forceinline__ void unpack8(const uint4& w, float (&v)[8], const __half*) {

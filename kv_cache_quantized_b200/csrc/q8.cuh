@@ -48,6 +48,21 @@ __device__ __forceinline__ uint32_t q8_pack4(const float* y) {
   }
 }
 
+// The same for finite values within the largest code's reach (up to its rounding): no clamps, no NaN.
+template <bool I8>
+__device__ __forceinline__ uint32_t q8_pack4_finite(const float* y) {
+  if constexpr (I8) {
+    const uint32_t a = __byte_perm(__float2int_rn(y[0]), __float2int_rn(y[1]), 0x0040);
+    const uint32_t b = __byte_perm(__float2int_rn(y[2]), __float2int_rn(y[3]), 0x0040);
+    return __byte_perm(a, b, 0x5410);
+  } else {
+    uint16_t lo, hi;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(y[1]), "f"(y[0]));
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(y[3]), "f"(y[2]));
+    return static_cast<uint32_t>(lo) | (static_cast<uint32_t>(hi) << 16);
+  }
+}
+
 // 4 codes to 4 values in fp16 (exact: integers up to 127, or 4 significant bits within fp16's range), as two half2.
 template <bool I8>
 __device__ __forceinline__ void q8_halves(uint32_t w, uint32_t& lo, uint32_t& hi) {

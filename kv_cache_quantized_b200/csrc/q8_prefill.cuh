@@ -8,7 +8,7 @@
 //   O += P V      A = P from tensor memory, B = the value codes in shared memory (fp16, N-major: token rows as they
 //                 lie in the cache), O in tensor memory, fp32.
 // Steps of 64 keys leave room for the second S: the scores of step i + 1 are there before the softmax of step i is done,
-// and no product waits for another's end (one S of 128 keys a row tile: 1093 us, two of 64: see below).
+// and no product waits for another's end.
 // Codes turn into fp16 exactly, so the scales of the 16-token blocks never touch the operands: ks goes into the
 // exponent's multiplier and vs, as log2 vs, into its offset, one pair for 16 columns; the normaliser takes vs back out
 // of each 16-column sum.  log2 vs counts relative to lref, the running maximum over tiles rounded up, and not below
@@ -23,6 +23,13 @@
 // when it grows by more than 2^kLazy (weights stay below 2^kLazy, and inside fp16 with the 2^(15 - kLazy) they are
 // scaled by), so the output is seldom rescaled, and a tile takes one pass over S: the weights are formed with the
 // present maximum and kept in registers until the tile's own maximum is known.
+//
+// Measured, 4 sequences x 2048 query tokens over up to 8192 keys, 32 / 8 heads, d = 128 (0.96 Tflop): 930-980 us, about
+// 1.0 PFLOP/s, 0.61-0.64 of the bf16 GEMM rate.  Nothing is saturated: tensor pipe 52 %, exponentials 53 %, issue slots
+// 56 % of the active cycles; without its MMAs, its exponentials or its conversions the kernel is 6-9 % faster each, so
+// the chain of hand-overs (a satisfied mbarrier wait costs a warp about 170 clocks) bounds it.  Slower forms: one S of 128
+// keys a row tile (1093 us), one issuing warp for all products (1366 us), one a row tile (1024 us), all 64 columns of a
+// step loaded at once (1044 us), two threads a row (1124 us).
 #pragma once
 
 #include "q8_attend.cuh"
