@@ -381,6 +381,7 @@ AXR_API axr_status axr_pot_attend_decode(const float* q, const uint8_t* codes, c
  *   cu_new/cu_q  [dev] [B + 1] int32, non-decreasing: sequence b's tokens are cu[b] .. cu[b + 1] - 1; NULL: one token
  *                per sequence (n_tok = B).  Tokens at or past cu[B] belong to no sequence: nothing of theirs is read
  *                into the cache, and their output rows are left as they are;
+ *                B at most 2^14;
  *   seq_lens     [dev] [B] int32, lengths with the new tokens: token i of sequence b has cache position
  *                seq_lens[b] - (cu[b + 1] - cu[b]) + (i - cu[b]);
  *   block_table  [dev] [B, max_blocks] int32, pool block of each logical block; block_tokens a power of two in
@@ -393,7 +394,8 @@ AXR_API axr_status axr_pot_attend_decode(const float* q, const uint8_t* codes, c
  *   q_out        [dev] out, the rotated queries, contiguous; NULL together with q.
  * Tokens whose cache position is negative are skipped.  Tokens past the block table's reach, with a table entry outside
  * [0, num_blocks) or a rotation position outside [0, max_pos) are skipped and set AXR_STATUS_BAD_INDEX.  No two
- * sequences may have new tokens in one pool block.  Inputs must be finite: in the 8-bit cache NaN is held as 0 and an
+ * sequences may have new tokens in one pool block, nor may a block that another sequence reads get new tokens (its older
+ * codes may be rounded again; copy it first).  Inputs must be finite: in the 8-bit cache NaN is held as 0 and an
  * infinity as the block's largest code (neither counts towards its scale).
  *
  * axr_append_paged -- keys through the write path of axr_write_keys on the rotated key (the same codes and norms, bit

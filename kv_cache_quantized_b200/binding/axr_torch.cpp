@@ -90,6 +90,12 @@ int64_t integer(PyObject* o) {
   return v;
 }
 
+bool truth(PyObject* o) {
+  const int v = PyObject_IsTrue(o);
+  if (v < 0) throw Refused();
+  return v != 0;
+}
+
 // axr statuses become the package's AxrError.
 void check(axr_status st, const char* what) {
   if (st == AXR_OK) return;
@@ -190,6 +196,7 @@ PyObject* append_paged(PyObject*, PyObject* const* a, Py_ssize_t na) {
     NewTokens nt(a[0], a[1], a[6], a[7], a[8], a[9], a[10], a[11], a[16], true);
     const at::Tensor &kc = *tensor(a[2], "kcodes"), &kn = *tensor(a[3], "knorms"), &sg = *tensor(a[4], "signs");
     const int64_t bits = integer(a[5]);
+    const int interleaved = truth(a[12]) ? 1 : 0;
     need_cuda(kc, "kcodes", at::kByte);
     need_cuda(kn, "knorms", at::kHalf);
     need_cuda(sg, "signs", at::kChar);
@@ -216,7 +223,7 @@ PyObject* append_paged(PyObject*, PyObject* const* a, Py_ssize_t na) {
     check(axr_append_paged(
               ptr(nt.q), ptr(nt.k), ptr(nt.v), nt.dtype(), nt.qs, nt.ks, nt.vs,
               static_cast<const float*>(ptr(nt.rope)), nt.max_pos, static_cast<int>(nt.rot),
-              PyObject_IsTrue(a[12]) ? 1 : 0, static_cast<const int32_t*>(ptr(nt.pos)),
+              interleaved, static_cast<const int32_t*>(ptr(nt.pos)),
               static_cast<const int32_t*>(ptr(nt.cu)), static_cast<const int32_t*>(ptr(nt.lens)), nt.n,
               static_cast<int>(nt.B), static_cast<int>(nt.Hq), static_cast<int>(nt.Hkv), static_cast<int>(nt.d),
               static_cast<int>(bits), static_cast<const int8_t*>(ptr(&sg)), static_cast<uint8_t*>(mut(&kc)),
@@ -266,13 +273,14 @@ PyObject* q8_append_paged(PyObject*, PyObject* const* a, Py_ssize_t na) {
   try {
     NewTokens nt(a[0], a[1], a[6], a[7], a[9], a[10], a[11], a[12], a[14], false);
     const Pools8 p(a + 2);
+    const int interleaved = truth(a[13]) ? 1 : 0;
     if (p.Hkv != nt.Hkv || p.d != nt.d) refuse(PyExc_ValueError, "the pools do not match the new tokens' heads");
     same_device(*nt.k, {p.kc, p.ks, p.vc, p.vs});
     const c10::cuda::CUDAGuard guard(nt.k->device());
     check(axr_q8_append_paged(
               ptr(nt.q), ptr(nt.k), ptr(nt.v), nt.dtype(), nt.qs, nt.ks, nt.vs,
               static_cast<const float*>(ptr(nt.rope)), nt.max_pos, static_cast<int>(nt.rot),
-              PyObject_IsTrue(a[13]) ? 1 : 0, static_cast<const int32_t*>(ptr(nt.pos)),
+              interleaved, static_cast<const int32_t*>(ptr(nt.pos)),
               static_cast<const int32_t*>(ptr(nt.cu)), static_cast<const int32_t*>(ptr(nt.lens)), nt.n,
               static_cast<int>(nt.B), static_cast<int>(nt.Hq), static_cast<int>(nt.Hkv), static_cast<int>(nt.d),
               static_cast<int>(integer(a[8])), static_cast<uint8_t*>(mut(p.kc)), static_cast<float*>(mut(p.ks)),

@@ -27,6 +27,9 @@ inline axr_status check_table(const char* w, const int32_t* table, int max_block
   return AXR_OK;
 }
 
+// Every warp scans the batch's entries, 32 a round trip, so that a call's time has a part that grows as B^2.
+constexpr int kMaxSeqs = 1 << 14;
+
 inline size_t dtype_bytes(axr_dtype t) { return t == AXR_F32 ? 4 : 2; }
 
 // Everything but the pools.  Fills p (its status word through paged_new_status, the only CUDA call).
@@ -38,8 +41,9 @@ inline axr_status paged_new_args(const char* w, const void* q, const void* k, co
                                  int num_blocks, const void* q_out, PagedNew* p) {
   if (x_dtype != AXR_F32 && x_dtype != AXR_F16 && x_dtype != AXR_BF16)
     return set_error(AXR_EINVAL, "%s: bad dtype", w);
-  if (n_tok < 0 || n_tok > 0x7fffffff || B < 0 || B > (1 << 24) || Hkv <= 0 || Hkv > 65535)
+  if (n_tok < 0 || n_tok > 0x7fffffff || B < 0 || Hkv <= 0 || Hkv > 65535)
     return set_error(AXR_EINVAL, "%s: bad sizes n_tok=%lld B=%d Hkv=%d", w, static_cast<long long>(n_tok), B, Hkv);
+  if (B > kMaxSeqs) return set_error(AXR_EUNSUPPORTED, "%s: B=%d above %d sequences", w, B, kMaxSeqs);
   if (d != 64 && d != 128) return set_error(AXR_EUNSUPPORTED, "%s: d=%d not in {64,128}", w, d);
   if ((q == nullptr) != (q_out == nullptr)) return set_error(AXR_EINVAL, "%s: q and q_out go together", w);
   if (q && (Hq <= 0 || Hq % Hkv))

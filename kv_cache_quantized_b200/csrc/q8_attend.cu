@@ -75,9 +75,10 @@ bool one_tile(bool ragged, int max_q, int G) { return !ragged || (max_q > 0 && s
 
 extern "C" size_t axr_q8_attend_workspace_bytes(int64_t n_tok, int max_q, int B, int Hq, int Hkv, int T, int d) {
   using namespace axr;
-  if (n_tok <= 0 || n_tok > 0x7fffffff || B <= 0 || Hkv <= 0 || Hq <= 0 || Hq % Hkv || Hq / Hkv > 16 || T <= 0 ||
-      d <= 0 || max_q < 0)
+  if (n_tok <= 0 || n_tok > 0x7fffffff || B <= 0 || Hkv <= 0 || Hq <= 0 || Hq % Hkv || Hq / Hkv > 16 || T < 0 ||
+      d <= 0 || max_q < 0 || B > kMaxSeqs)
     return 0;
+  if (T == 0) T = 1;
   const int G = Hq / Hkv;
   if (max_q == 0 || max_q > n_tok) max_q = static_cast<int>(n_tok);
   const bool one = one_tile(true, max_q, G);
@@ -97,10 +98,11 @@ extern "C" axr_status axr_q8_attend_paged(const void* q, axr_dtype x_dtype, int6
   if (x_dtype != AXR_F32 && x_dtype != AXR_F16 && x_dtype != AXR_BF16)
     return set_error(AXR_EINVAL, "%s: bad dtype", w);
   if (kind != AXR_Q8_INT && kind != AXR_Q8_E4M3) return set_error(AXR_EINVAL, "%s: bad kind %d", w, kind);
-  if (n_tok < 0 || n_tok > 0x7fffffff || B < 0 || B > (1 << 24) || Hq <= 0 || Hkv <= 0 || Hkv > 65535 || T < 0 ||
+  if (n_tok < 0 || n_tok > 0x7fffffff || B < 0 || Hq <= 0 || Hkv <= 0 || Hkv > 65535 || T < 0 ||
       max_q < 0)
     return set_error(AXR_EINVAL, "%s: bad sizes n_tok=%lld max_q=%d B=%d Hq=%d Hkv=%d T=%d", w,
                      static_cast<long long>(n_tok), max_q, B, Hq, Hkv, T);
+  if (B > kMaxSeqs) return set_error(AXR_EUNSUPPORTED, "%s: B=%d above %d sequences", w, B, kMaxSeqs);
   if (Hq % Hkv) return set_error(AXR_EINVAL, "%s: Hq=%d is not a multiple of Hkv=%d", w, Hq, Hkv);
   if (d != 64 && d != 128) return set_error(AXR_EUNSUPPORTED, "%s: d=%d not in {64,128}", w, d);
   const int G = Hq / Hkv;
@@ -136,7 +138,8 @@ extern "C" axr_status axr_q8_attend_paged(const void* q, axr_dtype x_dtype, int6
   const bool one = one_tile(cu_q != nullptr, max_q, G), prefill = !one && x_dtype != AXR_F32;
   const Q8Plan pl = prefill ? plan_prefill(n_tok, B, G, Hkv, T > 0 ? T : 1)
                             : plan_decode(n_tok, B, G, Hkv, T > 0 ? T : 1, one, max_q);
-  if (pl.tl.tiles * Hkv * 8 * pl.nrg > 0x7fffffff || pl.tl.tiles * Hkv * pl.sp.splits > 0x7fffffff) return set_error(AXR_EUNSUPPORTED, "%s: too many rows", w);
+  if (pl.tl.tiles * Hkv * 8 * pl.nrg > 0x7fffffff || pl.tl.tiles * Hkv * pl.sp.splits > 0x7fffffff)
+    return set_error(AXR_EUNSUPPORTED, "%s: too many rows", w);
   a.splits = pl.sp.splits;
   a.chunk = pl.sp.chunk;
   const size_t need = partial_bytes(pl, d);

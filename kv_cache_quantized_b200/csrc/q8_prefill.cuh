@@ -515,7 +515,7 @@ q8_prefill_kernel(const __grid_constant__ Q8Attend a, const Q8Tiles tl) {
     const bool live = threadIdx.x < nrow;
     const float nan = __uint_as_float(0x7fc00000u);
     const float unscale = ex2(lref - static_cast<float>(15 - kLazy));
-    const float f = a.splits == 1 ? (l > 0.f ? unscale / l : 0.f) : unscale;
+    const float f = a.splits == 1 ? (l == 0.f ? 0.f : unscale / l) : unscale;  // NaN stays
     const int64_t part = ((tile * a.Hkv + hk) * kQ8PrefillRows + threadIdx.x) * a.splits + split;
 #pragma unroll 1
     for (int k = 0; k < D / 16; ++k) {
@@ -525,7 +525,7 @@ q8_prefill_kernel(const __grid_constant__ Q8Attend a, const Q8Tiles tl) {
         tc::ld_x16(to + 16 * k, o);
         tc::wait_ld();
 #pragma unroll
-        for (int e = 0; e < 16; ++e) x[e] = l > 0.f ? __uint_as_float(o[e]) * f : 0.f;
+        for (int e = 0; e < 16; ++e) x[e] = l == 0.f ? 0.f : __uint_as_float(o[e]) * f;
       } else {
 #pragma unroll
         for (int e = 0; e < 16; ++e) x[e] = ok ? 0.f : nan;

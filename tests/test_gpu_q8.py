@@ -611,3 +611,43 @@ def test_two_graphs_that_share_a_workspace():
     with pytest.raises(_abi.AxrError) as e:
         ops.q8_attend_paged(a.q, *pa, a.t["table"], a.t["lens"], T=960, workspace=ws[:64])
     assert e.value.status == 4
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16", "f32"])
+@pytest.mark.parametrize("counts,max_q", [([1, 1, 1], 1), ([30, 80, 64], 80)])
+def test_a_query_row_that_is_not_finite_stays_alone(dtype, counts, max_q):
+    """NaN and infinite queries give NaN in their own rows and change no others."""
+    Hq, Hkv, d, bt = 8, 2, 128, 32
+    bt_ = Batch(counts, [500, 81, 300], Hq, Hkv, d, bt, dtype, 77, pad=0)
+    pools = [cuda(p) for p in filled(bt_, "i8")]
+    args = pools + [bt_.t["table"], bt_.t["lens"]]
+    good = ops.q8_attend_paged(bt_.q, *args, cu_q=bt_.t["cu"], max_q=max_q)
+    q = bt_.q.clone()
+    rows = [(0, 3, 5, math.nan), (bt_.n_tok - 1, 7, 64, math.inf)]
+    for i, h, j, x in rows:
+        q[i, h, j] = x
+    got = ops.q8_attend_paged(q, *args, cu_q=bt_.t["cu"], max_q=max_q)
+    keep = torch.ones(got.shape[:2], dtype=torch.bool, device="cuda")
+    for i, h, _, _ in rows:
+        assert torch.isnan(got[i, h]).all(), (i, h)
+        keep[i, h] = False
+    assert torch.equal(got[keep], good[keep])
+
+
+@pytest.mark.parametrize("counts", [[1, 1], [40, 90]])
+def test_an_axis_of_no_tokens(counts):
+    bt_ = Batch(counts, [64, 96], 8, 2, 64, 32, "bf16", 8, pad=0)
+    pools = [cuda(p) for p in filled(bt_, "i8")]
+    out = ops.q8_attend_paged(bt_.q, *pools, bt_.t["table"], bt_.t["lens"], cu_q=bt_.t["cu"], max_q=max(counts), T=0)
+    assert (out == 0).all()
+
+
+def test_interleaved_takes_a_truth_value():
+    bt_ = Batch([1, 1], [40, 40], 8, 2, 128, 32, "f16", 13, pad=0)
+    pools = [cuda(p) for p in filled(bt_, "i8")]
+    before = [p.clone() for p in pools]
+    with pytest.raises(RuntimeError):
+        ops.q8_append_paged(bt_.k, bt_.v, *pools, bt_.t["table"], bt_.t["lens"],
+                            cos_sin=cuda(rope_table(64, 128)), interleaved=torch.zeros(2))
+    torch.cuda.synchronize()
+    assert same(pools, before)

@@ -102,6 +102,7 @@ def test_q8_append_argument_errors(L):
     assert _append8(L, ks=128) == 1 and _append8(L, kc=None) == 1 and _append8(L, kc=FAKE + 4) == 1
     assert _append8(L, lens=None) == 1 and _append8(L, mp=0) == 1 and _append8(L, mb=(1 << 25) + 1) == 1
     assert _append8(L, n=0, B=0) == 0
+    assert _append8(L, n=16385, B=16385) == 2 and b"sequences" in L.axr_last_error()
 
 
 def test_append_argument_errors(L):
@@ -129,3 +130,7 @@ def test_q8_attend_argument_errors(L):
     assert need > 0 and call(ws=FAKE, wsb=need - 1) == 4 and call(ws=FAKE + 8, wsb=need) == 1
     assert call(n=0, B=0) == 0
     assert L.axr_q8_attend_workspace_bytes(0, 1, 2, 8, 2, 9000, 128) == 0
+    # T = 0 (every sequence cut to nothing) is a call like others, and its workspace is what the call asks for
+    need = L.axr_q8_attend_workspace_bytes(2, 1, 2, 8, 2, 0, 128)
+    assert need > 0 and call(T=0, ws=FAKE, wsb=need - 1) == 4 and call(T=0, ws=FAKE + 8, wsb=need) == 1
+    assert call(n=16385, B=16385) == 2 and L.axr_q8_attend_workspace_bytes(16385, 1, 16385, 8, 2, 9000, 128) == 0
