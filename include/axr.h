@@ -417,12 +417,12 @@ AXR_API axr_status axr_pot_attend_decode(const float* q, const uint8_t* codes, c
  *
  * axr_q8_attend_paged -- causal attention of the query tokens over the 8-bit cache that holds them already: token i of
  *   sequence b sees the cache positions up to its own.  out [n_tok, Hq, d] of x_dtype.  Sums and softmax statistics
- *   are fp32, codes enter the tensor cores exactly.  Up to 16 query rows (tokens x heads of a group) a sequence, and all
- *   fp32 calls: fp32 queries, and the weights of fp16 and fp32 calls, enter as hi and lo fp16 planes (about 22 bits).
- *   More rows of 16-bit queries: one fp16 plane each (2^-11 a weight).  A token that sees
+ *   are fp32, codes enter the tensor cores exactly.  fp32 queries and weights enter as hi and lo fp16 planes (about 22
+ *   bits), 16-bit ones as one fp16 plane (2^-11 a weight); calls of up to 16 query rows (tokens x heads of a group) a
+ *   sequence, and short sequences among long ones, keep two planes for the weights of fp16 calls.  A token that sees
  *   nothing (seq_lens[b] smaller than its sequence's token count) gets 0.
- *   max_q an upper bound of a sequence's query tokens, or 0 if unknown; rows of a longer sequence are not written (and
- *   AXR_STATUS_BAD_INDEX is set).  T an upper bound of the lengths (longer ones are cut to it); seq_lens NULL: all T.
+ *   max_q an upper bound of a sequence's query tokens, or 0 if unknown (a tight one picks the better kernel); rows of a
+ *   sequence with more may stay unwritten, which sets AXR_STATUS_BAD_INDEX.  T an upper bound of the lengths (longer ones are cut to it); seq_lens NULL: all T.
  *   A table entry outside [0, num_blocks) reads block 0 and sets AXR_STATUS_BAD_INDEX.  Cache rows at or past a
  *   sequence's length may hold anything.  G = Hq / Hkv in 1 .. 16.
  *   workspace [dev] >= axr_q8_attend_workspace_bytes(n_tok, max_q, B, Hq, Hkv, T, d) bytes (max_q = 1 without cu_q),

@@ -1,4 +1,5 @@
 // axr_q8_attend_paged: argument checks, the choice of kernels and the split of the token axis.
+#include <algorithm>
 #include <cmath>
 
 #include "axr_host.h"
@@ -16,6 +17,17 @@ struct Q8Plan {
   SplitPlan sp;   // q8_prefill
   size_t parts;   // partial rows in the workspace
 };
+
+// Sequences of few query rows among longer ones (decoding sequences in a batch of prompt chunks): the warp-MMA kernel
+// takes those of up to 8 rows (one token from 8 heads of a group on) and the tcgen05 kernel, which would run a 256-row
+// tile for each, the others.  The host knows no lengths, so the second launch is made where the mean length is below
+// half of the longest (32 / 8 heads, d = 128, bf16: 63 single tokens and a chunk of 512 on up to 4096 keys 199 -> 154 us,
+// 31 and a chunk of 2048 186 -> 167 us, 32 single tokens without a bound on max_q 96 -> 43 us; four ragged chunks, none
+// of them short, 176 -> 179 us).
+int short_tokens(int64_t n_tok, int B, int max_q, int G) {
+  if (2 * n_tok >= static_cast<int64_t>(B) * max_q) return 0;
+  return G <= 8 ? 8 / G : 1;
+}
 
 // The warp-MMA kernel: one block per SM, fewer when shares of two key tiles would not fill them.
 Q8Plan plan_decode(int64_t n_tok, int B, int G, int Hkv, int T, bool one, int max_q) {
@@ -83,8 +95,11 @@ extern "C" size_t axr_q8_attend_workspace_bytes(int64_t n_tok, int max_q, int B,
   if (max_q == 0 || max_q > n_tok) max_q = static_cast<int>(n_tok);
   const bool one = one_tile(true, max_q, G);
   const size_t x = partial_bytes(plan_decode(n_tok, B, G, Hkv, T, one, max_q), d);
-  const size_t y = one ? 0 : partial_bytes(plan_prefill(n_tok, B, G, Hkv, T), d);
-  return x > y ? x : y;
+  if (one) return x;
+  const int few = short_tokens(n_tok, B, max_q, G);
+  const size_t y = partial_bytes(plan_prefill(n_tok, B, G, Hkv, T), d);
+  const size_t z = few ? partial_bytes(plan_decode(n_tok, B, G, Hkv, T, true, few), d) : 0;
+  return std::max({x, y, z});
 }
 
 extern "C" axr_status axr_q8_attend_paged(const void* q, axr_dtype x_dtype, int64_t q_stride, const uint8_t* kcodes,
@@ -136,24 +151,42 @@ extern "C" axr_status axr_q8_attend_paged(const void* q, axr_dtype x_dtype, int6
   // up to 16 query rows per sequence and KV head: the warp-MMA kernel, one tile a sequence; more: the tcgen05 kernel,
   // or, for fp32 queries and outputs (which its fp16 weights could not serve), the warp-MMA kernel over flat tiles
   const bool one = one_tile(cu_q != nullptr, max_q, G), prefill = !one && x_dtype != AXR_F32;
-  const Q8Plan pl = prefill ? plan_prefill(n_tok, B, G, Hkv, T > 0 ? T : 1)
-                            : plan_decode(n_tok, B, G, Hkv, T > 0 ? T : 1, one, max_q);
-  if (pl.tl.tiles * Hkv * 8 * pl.nrg > 0x7fffffff || pl.tl.tiles * Hkv * pl.sp.splits > 0x7fffffff)
-    return set_error(AXR_EUNSUPPORTED, "%s: too many rows", w);
-  a.splits = pl.sp.splits;
-  a.chunk = pl.sp.chunk;
-  const size_t need = partial_bytes(pl, d);
+  Q8Plan pl = prefill ? plan_prefill(n_tok, B, G, Hkv, T > 0 ? T : 1)
+                      : plan_decode(n_tok, B, G, Hkv, T > 0 ? T : 1, one, max_q);
+  Q8Plan few;  // the short sequences' plan, beside pl
+  int few_tokens = prefill ? short_tokens(n_tok, B, max_q, G) : 0;
+  if (few_tokens) {
+    few = plan_decode(n_tok, B, G, Hkv, T > 0 ? T : 1, true, few_tokens);
+    few.tl.skip_long = true;
+    pl.tl.skip_short = few_tokens = few.tl.tpt;
+  }
+  const auto too_many = [&](const Q8Plan& x) {
+    return x.tl.tiles * Hkv * 8 * x.nrg > 0x7fffffff || x.tl.tiles * Hkv * x.sp.splits > 0x7fffffff;
+  };
+  if (too_many(pl) || (few_tokens && too_many(few))) return set_error(AXR_EUNSUPPORTED, "%s: too many rows", w);
+  // the two kernels of a mixed batch run after one another and share the workspace
+  const size_t need = std::max(partial_bytes(pl, d), few_tokens ? partial_bytes(few, d) : 0);
   if (need) {
     if (!workspace || ws_bytes < need)
       return set_error(AXR_EWORKSPACE, "%s: workspace of %zu bytes, need %zu", w, workspace ? ws_bytes : 0, need);
     if (!aligned(workspace, 16)) return set_error(AXR_EINVAL, "%s: workspace not 16-byte aligned", w);
-    a.ws_o = static_cast<float*>(workspace);
-    a.ws_m = a.ws_o + pl.parts * d;
-    a.ws_l = a.ws_m + pl.parts;
   }
   a.status = status_word();
   if (!a.status) return set_error(AXR_ECUDA, "%s: the status word has no device address", w);
+  const auto use = [&](const Q8Plan& x) {
+    a.splits = x.sp.splits;
+    a.chunk = x.sp.chunk;
+    a.ws_o = static_cast<float*>(workspace);
+    a.ws_m = a.ws_o + x.parts * d;
+    a.ws_l = a.ws_m + x.parts;
+  };
   cudaStream_t s = as_stream(stream);
+  if (few_tokens) {
+    use(few);
+    st = q8_decode_launch(x_dtype, d, kind == AXR_Q8_INT, few.nrg, few.grid, a, few.tl, s, w);
+    if (st != AXR_OK) return st;
+  }
+  use(pl);
   if (prefill) return q8_prefill_launch(x_dtype == AXR_F16, d, kind == AXR_Q8_INT, a, pl.tl, s, w);
   return q8_decode_launch(x_dtype, d, kind == AXR_Q8_INT, pl.nrg, pl.grid, a, pl.tl, s, w);
 }

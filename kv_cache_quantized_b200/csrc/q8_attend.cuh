@@ -55,7 +55,8 @@ __device__ __forceinline__ Q8Span q8_span(const Q8Attend& a, int b) {
 //  one  = true:  tile b is sequence b, which has at most tpt tokens; longer sequences are another kernel's (skip_long)
 //                or break the caller's bound (flagged in the status word);
 //  one  = false: sequence b owns the tiles from cu[b] / tpt + b on: at most n_tok / tpt + B tiles in all, found
-//                without knowing the lengths on the host.  Sequences of at most skip_short tokens are skipped.
+//                without knowing the lengths on the host.  Sequences of at most skip_short tokens are skipped (another
+//                kernel's).
 struct Q8Tiles {
   int64_t tiles;
   int tpt;

@@ -651,3 +651,22 @@ def test_interleaved_takes_a_truth_value():
                             cos_sin=cuda(rope_table(64, 128)), interleaved=torch.zeros(2))
     torch.cuda.synchronize()
     assert same(pools, before)
+
+
+@pytest.mark.parametrize("dtype,Hq,Hkv,kind", [("bf16", 8, 2, "i8"), ("f16", 16, 1, "e4m3"), ("f16", 3, 3, "i8")])
+@pytest.mark.parametrize("counts", [[1, 1, 90, 0, 2, 1, 3, 1, 8, 9, 17, 1], [129, 100, 1, 90, 120], [1, 300], [300, 1, 2]])
+def test_short_sequences_among_long_ones(dtype, Hq, Hkv, kind, counts):
+    """Batches that both attention kernels share and batches that one takes, with a workspace of the size asked for."""
+    lens = [n + 37 * i % 411 for i, n in enumerate(counts)]
+    bt_ = Batch(counts, lens, Hq, Hkv, 128, 32, dtype, 91)
+    pools = filled(bt_, kind)
+    out = torch.full((bt_.n_tok, Hq, 128), 55.0, dtype=DT[dtype], device="cuda")
+    T, mq = max(lens), max(counts)
+    need = ops.q8_attend_workspace_bytes(bt_.n_tok, mq, len(lens), Hq, Hkv, T, 128)
+    ws = torch.empty(need, dtype=torch.uint8, device="cuda")
+    ops.device_status(clear=True)
+    ops.q8_attend_paged(bt_.q, *[cuda(p) for p in pools], bt_.t["table"], bt_.t["lens"], kind=kind, cu_q=bt_.t["cu"],
+                        max_q=mq, T=T, out=out, workspace=ws)
+    assert ops.device_status() == 0
+    check_attention(out, bt_, [bt_.rows(bt_.qn, b) for b in range(len(lens))], pools, kind, 1 / math.sqrt(128), dtype,
+                    out_fill=55.0)
