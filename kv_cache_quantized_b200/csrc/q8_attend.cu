@@ -46,25 +46,35 @@ Q8Plan plan_decode(int64_t n_tok, int B, int G, int Hkv, int T, bool one, int ma
   return pl;
 }
 
-// The tcgen05 kernel: tiles of 256 rows, one thread block per SM.  In units of one key tile (128 tokens), a block's
-// set-up (query operand, first code tiles) costs about 2, and writing and merging the partials of a split axis about 3
-// more: its 256 x d fp32 rows cross HBM twice.
-Q8Plan plan_prefill(int64_t n_tok, int B, int G, int Hkv, int T) {
+// The tcgen05 kernel: tiles of 256 rows, one thread block per SM, a tile a sequence where max_q allows it.  In units of
+// one key tile (128 tokens), a block's set-up (query operand, first code tiles) costs about 2, and writing and merging
+// the partials of a split axis up to 3 more: a full tile's 256 x d fp32 rows cross HBM twice.  The host knows no
+// lengths: how many tiles have work is estimated, with every sequence, or, beside a launch for those of up to `few`
+// tokens, as many longer ones as there must be.  (A count of the numbered tiles instead of those with work split 148 units of 64 key tiles in
+// four: 173 against 115 us.)
+Q8Plan plan_prefill(int64_t n_tok, int B, int G, int Hkv, int T, int max_q, int few) {
   Q8Plan pl;
   pl.nrg = kQ8PrefillRows / 8;
   pl.tl.tpt = kQ8PrefillRows / G;
-  pl.tl.one = false;
+  pl.tl.one = max_q <= pl.tl.tpt;
   pl.tl.skip_long = false;
-  pl.tl.skip_short = 0;
-  pl.tl.tiles = n_tok / pl.tl.tpt + B;
-  const int64_t units = pl.tl.tiles * Hkv;
-  const int64_t total = (static_cast<int64_t>(T) + 127) / 128;
+  pl.tl.skip_short = few;
+  pl.tl.tiles = pl.tl.one ? B : n_tok / pl.tl.tpt + B;
+  const int64_t least = std::max<int64_t>(1, (n_tok - static_cast<int64_t>(few) * B + max_q - 1) / max_q);
+  const int64_t seqs = few ? least : B;
+  const int64_t live =
+      pl.tl.one ? seqs : std::min(n_tok / pl.tl.tpt + seqs, static_cast<int64_t>(B) * ((max_q - 1) / pl.tl.tpt + 1));
+  const int64_t units = live * Hkv, total = (static_cast<int64_t>(T) + 127) / 128;
+  const double fill = std::min(1.0, static_cast<double>(n_tok) * G / (static_cast<double>(live) * kQ8PrefillRows));
+  const auto waves = [&](int64_t s) { return static_cast<double>((units * s + kSmCount - 1) / kSmCount); };
+  // blocks without work take about 0.7 a wave
+  const double idle = 0.7 * static_cast<double>(pl.tl.tiles * Hkv - units) / kSmCount;
   pl.sp.splits = 1;
   pl.sp.chunk = static_cast<int>(total * 128);
-  int64_t best = ((units + kSmCount - 1) / kSmCount) * (total + 2);
+  double best = waves(1) * (total + 2) + idle;
   for (int64_t s = 2; s <= total / 2 && s <= 256; ++s) {
     const int64_t per = (total + s - 1) / s, splits = (total + per - 1) / per;
-    const int64_t cost = ((units * splits + kSmCount - 1) / kSmCount) * (per + 5);
+    const double cost = waves(splits) * (per + 2 + 3 * fill) + idle * splits;
     if (cost < best) {
       best = cost;
       pl.sp.splits = static_cast<int>(splits);
@@ -97,7 +107,7 @@ extern "C" size_t axr_q8_attend_workspace_bytes(int64_t n_tok, int max_q, int B,
   const size_t x = partial_bytes(plan_decode(n_tok, B, G, Hkv, T, one, max_q), d);
   if (one) return x;
   const int few = short_tokens(n_tok, B, max_q, G);
-  const size_t y = partial_bytes(plan_prefill(n_tok, B, G, Hkv, T), d);
+  const size_t y = partial_bytes(plan_prefill(n_tok, B, G, Hkv, T, max_q, few), d);
   const size_t z = few ? partial_bytes(plan_decode(n_tok, B, G, Hkv, T, true, few), d) : 0;
   return std::max({x, y, z});
 }
@@ -151,14 +161,13 @@ extern "C" axr_status axr_q8_attend_paged(const void* q, axr_dtype x_dtype, int6
   // up to 16 query rows per sequence and KV head: the warp-MMA kernel, one tile a sequence; more: the tcgen05 kernel,
   // or, for fp32 queries and outputs (which its fp16 weights could not serve), the warp-MMA kernel over flat tiles
   const bool one = one_tile(cu_q != nullptr, max_q, G), prefill = !one && x_dtype != AXR_F32;
-  Q8Plan pl = prefill ? plan_prefill(n_tok, B, G, Hkv, T > 0 ? T : 1)
-                      : plan_decode(n_tok, B, G, Hkv, T > 0 ? T : 1, one, max_q);
+  const int few_tokens = prefill ? short_tokens(n_tok, B, max_q, G) : 0;
+  const Q8Plan pl = prefill ? plan_prefill(n_tok, B, G, Hkv, T > 0 ? T : 1, max_q, few_tokens)
+                            : plan_decode(n_tok, B, G, Hkv, T > 0 ? T : 1, one, max_q);
   Q8Plan few;  // the short sequences' plan, beside pl
-  int few_tokens = prefill ? short_tokens(n_tok, B, max_q, G) : 0;
   if (few_tokens) {
     few = plan_decode(n_tok, B, G, Hkv, T > 0 ? T : 1, true, few_tokens);
     few.tl.skip_long = true;
-    pl.tl.skip_short = few_tokens = few.tl.tpt;
   }
   const auto too_many = [&](const Q8Plan& x) {
     return x.tl.tiles * Hkv * 8 * x.nrg > 0x7fffffff || x.tl.tiles * Hkv * x.sp.splits > 0x7fffffff;
@@ -176,6 +185,7 @@ extern "C" axr_status axr_q8_attend_paged(const void* q, axr_dtype x_dtype, int6
   const auto use = [&](const Q8Plan& x) {
     a.splits = x.sp.splits;
     a.chunk = x.sp.chunk;
+    a.rows = std::min(max_q, x.tl.tpt) * G;
     a.ws_o = static_cast<float*>(workspace);
     a.ws_m = a.ws_o + x.parts * d;
     a.ws_l = a.ws_m + x.parts;

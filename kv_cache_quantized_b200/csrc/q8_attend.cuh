@@ -25,6 +25,7 @@ struct Q8Attend {
   int64_t n_tok;
   int B, Hq, Hkv, G, T, max_blocks, shift, num_blocks;
   int splits, chunk;        // q8_prefill: the token axis as splits chunks of `chunk` tokens
+  int rows;                 // q8_prefill: rows that a tile has at most, by the caller's bound on the query tokens
   float mult;               // scale * log2 e
   unsigned int* status;
 };
@@ -85,6 +86,36 @@ __device__ __forceinline__ void q8_tile(const Q8Attend& a, const Q8Tiles& tl, in
     b = last_at_most(a.B, tile, lane, start);
     i0 = (tile - start(b)) * tl.tpt;
   }
+}
+
+// The same, and the sequence's entries, in one round trip to memory for every 32 sequences.
+__device__ __forceinline__ Q8Span q8_tile_span(const Q8Attend& a, const Q8Tiles& tl, int64_t tile, int lane, int& b,
+                                               int64_t& i0) {
+  if (tl.one) {
+    b = static_cast<int>(tile);
+    i0 = 0;
+    return q8_span(a, b);
+  }
+  Q8Span r{0, 0, 0, 0};
+  b = 0;
+  i0 = -1;
+#pragma unroll 2
+  for (int b0 = 0; b0 < a.B; b0 += 32) {
+    const int c = min(b0 + lane, a.B - 1);
+    const Q8Span s = q8_span(a, c);
+    const int64_t first = static_cast<int64_t>(a.cu[c] / tl.tpt) + c;
+    const unsigned who = __ballot_sync(0xffffffffu, b0 + lane < a.B && first <= tile);
+    if (who) {
+      const int src = 31 - __clz(who);
+      b = b0 + src;
+      i0 = (tile - __shfl_sync(0xffffffffu, first, src)) * tl.tpt;
+      r.first = __shfl_sync(0xffffffffu, s.first, src);
+      r.count = __shfl_sync(0xffffffffu, s.count, src);
+      r.pos0 = __shfl_sync(0xffffffffu, s.pos0, src);
+      r.len = __shfl_sync(0xffffffffu, s.len, src);
+    }
+  }
+  return r;
 }
 
 __device__ __forceinline__ bool q8_tile_live(const Q8Attend& a, const Q8Tiles& tl, const Q8Span& sp, int64_t i0,

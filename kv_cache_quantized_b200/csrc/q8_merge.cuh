@@ -89,28 +89,29 @@ __device__ __forceinline__ void q8_merge_row(const Q8Attend& a, int n, Part part
   static_cast<T*>(a.out)[orow * D + j] = from_float<T>(L == 0.f ? 0.f : x / L);
 }
 
-// Merge of q8_prefill_kernel's split partials: one block a row of a (row tile, KV head), or, for up to 8 splits, a warp.
-// Launched as a programmatic dependent of it.
+// Merge of q8_prefill_kernel's split partials, the first `rows` rows of each (row tile, KV head): a block a row, or, for
+// up to 8 splits, a warp `each` rows.  Launched as a programmatic dependent of it.
 template <typename T, int D, int NW>
 __global__ void __launch_bounds__(32 * kMergeWarps)
-q8_merge_kernel(const __grid_constant__ Q8Attend a, const __grid_constant__ Q8Tiles tl) {
-  const int64_t idx = NW == 1 ? static_cast<int64_t>(blockIdx.x) * kMergeWarps + (threadIdx.x >> 5) : blockIdx.x;
-  const int per = tl.tpt * a.G;
-  const int64_t unit = idx / per, tile = unit / a.Hkv;
-  const int r = static_cast<int>(idx - unit * per), hk = static_cast<int>(unit % a.Hkv);
+q8_merge_kernel(const __grid_constant__ Q8Attend a, const __grid_constant__ Q8Tiles tl, int rows, int each) {
+  const int per = NW == 1 ? kMergeWarps * each : 1, groups = (rows + per - 1) / per;
+  const int unit = static_cast<int>(blockIdx.x) / groups, r0 = static_cast<int>(blockIdx.x) % groups * per;
+  const int tile = unit / a.Hkv, hk = unit % a.Hkv;
   // every block waits, those without a row too: this grid's end stands for the attention kernel's
   const auto wait = [] { asm volatile("griddepcontrol.wait;\n" ::: "memory"); };
-  if (tile >= tl.tiles) return wait();
   int b;
   int64_t i0;
-  q8_tile(a, tl, tile, threadIdx.x & 31, b, i0);
-  const Q8Span sp = q8_span(a, b);
+  const Q8Span sp = q8_tile_span(a, tl, tile, threadIdx.x & 31, b, i0);
   if (!q8_tile_live(a, tl, sp, i0, threadIdx.x)) return wait();
-  if (r >= min(tl.tpt, sp.count - static_cast<int>(i0)) * a.G) return wait();
+  const int nrow = min(tl.tpt, sp.count - static_cast<int>(i0)) * a.G;
+  if (nrow > rows && r0 == 0 && threadIdx.x == 0) atomicOr(a.status, kStatusBadIndex);  // more tokens than max_q
   wait();  // the partials are complete and visible after this
-  const int64_t p0 = (unit * kQ8PrefillRows + r) * a.splits;
-  const int64_t orow = (sp.first + i0 + r / a.G) * a.Hq + static_cast<int64_t>(hk) * a.G + r % a.G;
-  q8_merge_row<T, D, NW>(a, a.splits, [&](int k) { return p0 + k; }, orow);
+  const int end = min(nrow, min(rows, r0 + per));
+  for (int r = r0 + (NW == 1 ? static_cast<int>(threadIdx.x) >> 5 : 0); r < end; r += kMergeWarps) {
+    const int64_t p0 = (static_cast<int64_t>(unit) * kQ8PrefillRows + r) * a.splits;
+    const int64_t orow = (sp.first + i0 + r / a.G) * a.Hq + static_cast<int64_t>(hk) * a.G + r % a.G;
+    q8_merge_row<T, D, NW>(a, a.splits, [&](int k) { return p0 + k; }, orow);
+  }
 }
 
 }  // namespace axr

@@ -16,9 +16,12 @@ axr_status launch(const Q8Attend& a, const Q8Tiles& tl, cudaStream_t st, const c
     auto merge = a.splits <= 8 ? q8_merge_kernel<T, D, 1> : q8_merge_kernel<T, D, kMergeWarps>;
     // the merge keeps the attention kernel's split of L1: another one would have to wait for every SM to drain
     cudaFuncSetAttribute(merge, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
-    const int64_t rows = tl.tiles * a.Hkv * tl.tpt * a.G;
+    // a warp a row until the warps fill the SMs, then up to 8 rows each: many tiles have no work
+    const int64_t units = tl.tiles * a.Hkv, warps = units * a.rows, resident = 64 * kSmCount;
+    const int each = static_cast<int>(warps <= resident ? 1 : warps < 8 * resident ? (warps + resident - 1) / resident : 8);
+    const int per = a.splits <= 8 ? kMergeWarps * each : 1;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(a.splits <= 8 ? (rows + kMergeWarps - 1) / kMergeWarps : rows));
+    cfg.gridDim = dim3(static_cast<unsigned>(units * ((a.rows + per - 1) / per)));
     cfg.blockDim = dim3(32 * kMergeWarps);
     cfg.stream = st;
     cudaLaunchAttribute attr[1];
@@ -26,7 +29,7 @@ axr_status launch(const Q8Attend& a, const Q8Tiles& tl, cudaStream_t st, const c
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    cudaLaunchKernelEx(&cfg, merge, a, tl);
+    cudaLaunchKernelEx(&cfg, merge, a, tl, a.rows, each);
   }
   return check_launch(w);
 }

@@ -161,8 +161,7 @@ q8_prefill_kernel(const __grid_constant__ Q8Attend a, const Q8Tiles tl) {
   const int64_t tile = idx / (static_cast<int64_t>(a.splits) * a.Hkv);
   int b;
   int64_t i0;
-  q8_tile(a, tl, tile, lane, b, i0);
-  const Q8Span sp = q8_span(a, b);
+  const Q8Span sp = q8_tile_span(a, tl, tile, lane, b, i0);
   if (!q8_tile_live(a, tl, sp, i0, lane)) return;  // uniform over the block
   const int ntok = min(tl.tpt, sp.count - static_cast<int>(i0)), nrow = ntok * a.G;
   const int nq = nrow > 128 ? 2 : 1;                             // row tiles in use

@@ -670,3 +670,31 @@ def test_short_sequences_among_long_ones(dtype, Hq, Hkv, kind, counts):
     assert ops.device_status() == 0
     check_attention(out, bt_, [bt_.rows(bt_.qn, b) for b in range(len(lens))], pools, kind, 1 / math.sqrt(128), dtype,
                     out_fill=55.0)
+
+
+@pytest.mark.parametrize("dtype,kind", [("bf16", "i8"), ("f16", "e4m3")])
+@pytest.mark.parametrize("counts,lens", [
+    ([250] + [1] * 30, [1500] + [37 * i % 1400 + 1 for i in range(30)]),   # a split axis, most tiles without work
+    ([5] * 12, [1000 + 40 * i for i in range(12)]),                        # one tile a sequence, a split axis
+    ([64, 65, 63, 10, 0, 64], [800, 65, 1200, 300, 9, 64])])               # row tiles that end on a token and behind it
+def test_long_axes_of_mixed_batches(dtype, kind, counts, lens):
+    bt_ = Batch(counts, lens, 8, 2, 128, 64, dtype, 93)
+    pools = filled(bt_, kind)
+    out = torch.full((bt_.n_tok, 8, 128), 55.0, dtype=DT[dtype], device="cuda")
+    ops.q8_attend_paged(bt_.q, *[cuda(p) for p in pools], bt_.t["table"], bt_.t["lens"], kind=kind, cu_q=bt_.t["cu"],
+                        max_q=max(counts), T=max(lens), out=out)
+    check_attention(out, bt_, [bt_.rows(bt_.qn, b) for b in range(len(lens))], pools, kind, 1 / math.sqrt(128), dtype,
+                    out_fill=55.0)
+
+
+def test_more_queries_than_max_q_on_a_split_axis_is_flagged():
+    bt_ = Batch([7, 9], [4000, 3000], 8, 2, 128, 64, "bf16", 94, pad=0)
+    pools = [cuda(p) for p in filled(bt_, "i8")]
+    args = pools + [bt_.t["table"], bt_.t["lens"]]
+    want = ops.q8_attend_paged(bt_.q, *args, cu_q=bt_.t["cu"], max_q=9)
+    assert ops.device_status(clear=True) == 0
+    out = torch.full_like(want, 55.0)
+    ops.q8_attend_paged(bt_.q, *args, cu_q=bt_.t["cu"], max_q=8, out=out)
+    assert ops.device_status(clear=True) == 2
+    assert torch.equal(out[:15], want[:15])  # the ninth token of the second sequence may or may not be written
+    assert torch.equal(out[15], want[15]) or (out[15] == 55.0).all()
