@@ -35,7 +35,7 @@ constexpr int kThreads = 128;
 constexpr int kWarps = kThreads / 32;
 
 // Codes of one row to its place.  A lane holds N = BITS d / 32 consecutive bits of the row's bitstream: whole bytes are
-// stored as they are; otherwise groups of lanes that fill BITS (or 1) 32-bit words OR their fields together.
+// stored as they are; otherwise neighbouring lanes join their fields to 32-bit words.
 template <int D, int BITS>
 __device__ __forceinline__ void store_codes(const int (&code)[D / 32], uint8_t* __restrict__ out, int lane) {
   constexpr int VPL = D / 32, N = VPL * BITS;
@@ -46,31 +46,32 @@ __device__ __forceinline__ void store_codes(const int (&code)[D / 32], uint8_t* 
     out[lane] = static_cast<uint8_t>(f);
   } else if constexpr (N == 16) {
     reinterpret_cast<uint16_t*>(out)[lane] = static_cast<uint16_t>(f);
+  } else if constexpr (N % 3 == 0) {
+    // fields of neighbouring lanes joined to pieces of 24 bits, P lanes apart; word w = bits [32 w, 32 w + 32) begins in
+    // piece w + w / 3 and ends in the next
+    constexpr int P = 24 / N;
+    static_assert((P & (P - 1)) == 0, "whole pieces from a power of two of lanes");
+#pragma unroll
+    for (int m = 1; m < P; m <<= 1) f |= __shfl_down_sync(0xffffffffu, f, m) << (m * N);
+    const int a = lane + lane / 3, r = 8 * (lane % 3);
+    const uint32_t lo = __shfl_sync(0xffffffffu, f, a * P), hi = __shfl_sync(0xffffffffu, f, a * P + P);
+    if (lane < N) reinterpret_cast<uint32_t*>(out)[lane] = (lo >> r) | (hi << (24 - r));
   } else {
-    constexpr int W = N % 3 == 0 ? 3 : 1;      // words of a group
-    constexpr int GL = 32 * W / N;             // its lanes
-    static_assert(GL * N == 32 * W && (GL & (GL - 1)) == 0, "whole words from a power of two of lanes");
-    const int pos = (lane & (GL - 1)) * N;
-    const uint64_t at = static_cast<uint64_t>(f) << (pos & 31);
-    uint32_t w[W];
+    constexpr int GL = 32 / N;                 // lanes of a word
+    static_assert(GL * N == 32, "whole words from a power of two of lanes");
+    uint32_t w = f << (lane % GL * N);
 #pragma unroll
-    for (int k = 0; k < W; ++k)
-      w[k] = pos >> 5 == k ? static_cast<uint32_t>(at) : (pos >> 5) + 1 == k ? static_cast<uint32_t>(at >> 32) : 0u;
-#pragma unroll
-    for (int m = 1; m < GL; m <<= 1)
-#pragma unroll
-      for (int k = 0; k < W; ++k) w[k] |= __shfl_xor_sync(0xffffffffu, w[k], m);
-    const int mine = lane & (GL - 1);
-    uint32_t x = w[0];
-#pragma unroll
-    for (int k = 1; k < W; ++k) x = mine == k ? w[k] : x;
-    if (mine < W) reinterpret_cast<uint32_t*>(out)[lane / GL * W + mine] = x;
+    for (int m = 1; m < GL; m <<= 1) w |= __shfl_xor_sync(0xffffffffu, w, m);
+    if (lane % GL == 0) reinterpret_cast<uint32_t*>(out)[lane / GL] = w;
   }
 }
 
+// Seven blocks an SM hide more of the butterflies' latency (1400 fp32 tokens of 12 heads, d = 64, b = 3: 14.2 -> 12.9 us;
+// 400 bf16 tokens of 8 heads, d = 128: 7.2 -> 6.1 us); long calls with quantized values of d = 128 want the registers of
+// six (4000 tokens of 8 heads: 36.0 against 36.7 us).
 // Units of work: kv_units of (token, KH KV heads), then (token, slice of query heads).
 template <typename T, int D, int BITS, bool VQ, int KH>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, KH == 4 && VQ && D == 128 ? 6 : 7)
 append_kernel(const __grid_constant__ PagedNew p, const __grid_constant__ AppendArgs a, int64_t kv_units, int kv_parts,
               int q_parts) {
   constexpr int VPL = D / 32, R = D * BITS / 8;
