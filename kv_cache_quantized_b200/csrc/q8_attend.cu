@@ -21,9 +21,9 @@ struct Q8Plan {
 // Sequences of few query rows among longer ones (decoding sequences in a batch of prompt chunks): the warp-MMA kernel
 // takes those of up to 8 rows (one token from 8 heads of a group on) and the tcgen05 kernel, which would run a 256-row
 // tile for each, the others.  The host knows no lengths, so the second launch is made where the mean length is below
-// half of the longest (32 / 8 heads, d = 128, bf16: 63 single tokens and a chunk of 512 on up to 4096 keys 199 -> 154 us,
-// 31 and a chunk of 2048 186 -> 167 us, 32 single tokens without a bound on max_q 96 -> 43 us; four ragged chunks, none
-// of them short, 176 -> 179 us).
+// half of the longest (32 / 8 heads, d = 128, bf16: 63 single tokens and a chunk of 512 on up to 4096 keys 199 -> 151 us,
+// 31 and a chunk of 2048 186 -> 165 us, 32 single tokens without a bound on max_q 96 -> 51 us; four ragged chunks, none
+// of them short, 3 us more).
 int short_tokens(int64_t n_tok, int B, int max_q, int G) {
   if (2 * n_tok >= static_cast<int64_t>(B) * max_q) return 0;
   return G <= 8 ? 8 / G : 1;
@@ -50,8 +50,9 @@ Q8Plan plan_decode(int64_t n_tok, int B, int G, int Hkv, int T, bool one, int ma
 // one key tile (128 tokens), a block's set-up (query operand, first code tiles) costs about 2, and writing and merging
 // the partials of a split axis up to 3 more: a full tile's 256 x d fp32 rows cross HBM twice.  The host knows no
 // lengths: how many tiles have work is estimated, with every sequence, or, beside a launch for those of up to `few`
-// tokens, as many longer ones as there must be.  (A count of the numbered tiles instead of those with work split 148 units of 64 key tiles in
-// four: 173 against 115 us.)
+// tokens, as many longer ones as there must be.  (A count of the numbered tiles instead of those with work split 148
+// units of 64 key tiles in four: 173 against 117 us.)  The workspace holds partials for every numbered tile, with work
+// or without, so a split stops at 16 blocks an SM: 315 MB at d = 128.
 Q8Plan plan_prefill(int64_t n_tok, int B, int G, int Hkv, int T, int max_q, int few) {
   Q8Plan pl;
   pl.nrg = kQ8PrefillRows / 8;
@@ -72,7 +73,7 @@ Q8Plan plan_prefill(int64_t n_tok, int B, int G, int Hkv, int T, int max_q, int 
   pl.sp.splits = 1;
   pl.sp.chunk = static_cast<int>(total * 128);
   double best = waves(1) * (total + 2) + idle;
-  for (int64_t s = 2; s <= total / 2 && s <= 256; ++s) {
+  for (int64_t s = 2; s <= total / 2 && s <= 256 && pl.tl.tiles * Hkv * s <= 16 * kSmCount; ++s) {
     const int64_t per = (total + s - 1) / s, splits = (total + per - 1) / per;
     const double cost = waves(splits) * (per + 2 + 3 * fill) + idle * splits;
     if (cost < best) {

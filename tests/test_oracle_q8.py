@@ -133,4 +133,7 @@ def test_q8_attend_argument_errors(L):
     # T = 0 (every sequence cut to nothing) is a call like others, and its workspace is what the call asks for
     need = L.axr_q8_attend_workspace_bytes(2, 1, 2, 8, 2, 0, 128)
     assert need > 0 and call(T=0, ws=FAKE, wsb=need - 1) == 4 and call(T=0, ws=FAKE + 8, wsb=need) == 1
+    # large batches and long axes do not multiply
+    assert 0 < L.axr_q8_attend_workspace_bytes(16500, 60, 16384, 32, 8, 1 << 20, 128) < 1 << 29
+    assert 0 < L.axr_q8_attend_workspace_bytes(4, 4, 1, 32, 2, 1 << 30, 128) < 1 << 29
     assert call(n=16385, B=16385) == 2 and L.axr_q8_attend_workspace_bytes(16385, 1, 16385, 8, 2, 9000, 128) == 0
