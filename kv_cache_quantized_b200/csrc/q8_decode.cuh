@@ -402,7 +402,8 @@ q8_decode_kernel(const __grid_constant__ Q8Attend a, const __grid_constant__ Q8T
 
       const float vmax = fmaxf(vs[0], vs[1]);
       if (vmax > vref) {  // uniform
-        const float up = __uint_as_float((__float_as_uint(vmax) + 0x7fffffu) & 0x7f800000u);
+        // the power of two at or above vmax, from 2^-126 (subnormal scales) to 2^127: its reciprocal is exact
+        const float up = __uint_as_float(min((__float_as_uint(vmax) + 0x7fffffu) & 0x7f800000u, 0x7f000000u));
         const float f = vref / up;
         vref = up;
 #pragma unroll
@@ -412,9 +413,10 @@ q8_decode_kernel(const __grid_constant__ Q8Attend a, const __grid_constant__ Q8T
 #pragma unroll
             for (int e = 0; e < 4; ++e) o[n][j][e] *= f;
       }
-      // weights are formed relative to vref and 2^14 up: at most 2^14 in fp16, the lo plane's last step 2^-24
-      const float vi = vref > 0.f ? 16384.f / vref : 0.f;
-      const float vf[2] = {vs[0] * vi, vs[1] * vi};
+      // weights are formed relative to vref and 2^14 up: at most 2^15 in fp16, the last plane's last step 2^-24
+      // 1 / vref by its exponent (2^-127 is subnormal); vref = 0 where every scale so far, these two too, was 0
+      const float vi = __uint_as_float(max(0x7f000000u - __float_as_uint(vref), 0x00400000u));
+      const float vf[2] = {vs[0] * vi * 16384.f, vs[1] * vi * 16384.f};
 
       uint32_t pf[NRG][PP][2][2];
 #pragma unroll
@@ -520,7 +522,7 @@ q8_decode_kernel(const __grid_constant__ Q8Attend a, const __grid_constant__ Q8T
     }
 
     // the rows' outputs, or their partials when the unit is cut
-    const float unscale = vref * (1.f / 16384.f);
+    const float unscale = 1.f / 16384.f;  // vref comes last: with it, the factor could leave fp32's normal range
 #pragma unroll
     for (int n = 0; n < NRG; ++n)
 #pragma unroll
@@ -534,8 +536,8 @@ q8_decode_kernel(const __grid_constant__ Q8Attend a, const __grid_constant__ Q8T
         float y[VB];
 #pragma unroll
         for (int j = 0; j < NO; ++j) {
-          y[2 * j] = whole && l == 0.f ? 0.f : o[n][j][r] * f;
-          y[2 * j + 1] = whole && l == 0.f ? 0.f : o[n][j][2 + r] * f;
+          y[2 * j] = whole && l == 0.f ? 0.f : o[n][j][r] * f * vref;
+          y[2 * j + 1] = whole && l == 0.f ? 0.f : o[n][j][2 + r] * f * vref;
         }
         if (whole) {
           const int64_t orow = (sp.first + i0 + row / a.G) * a.Hq + static_cast<int64_t>(hk) * a.G + row % a.G;

@@ -1,0 +1,88 @@
+"""Attention over the 8-bit cache at the ends of what a call may hold: value scales from fp32's smallest to its largest."""
+
+import math
+
+import numpy as np
+import pytest
+import torch
+
+from kv_cache_quantized_b200 import ops
+from oracle import q8
+from tests.test_gpu_q8 import DT, Batch, cuda, filled
+
+pytestmark = pytest.mark.gpu
+
+# one query token a sequence (the warp-MMA kernel), flat tiles of the same kernel (fp32), the tcgen05 kernel
+FORMS = [("f32", [1, 1, 1]), ("bf16", [1, 1, 1]), ("f16", [1, 1, 1]), ("f32", [30, 40, 64]), ("bf16", [30, 40, 64]),
+         ("f16", [30, 40, 64])]
+
+
+def uses_tcgen05(dtype, counts, G):
+    return dtype != "f32" and max(counts) * G > 16
+
+
+def check(got, bt_, pools, kind, scale, dtype, G):
+    """|o - ref| <= (4 delta + (T / 16 + 64) 2^-23 + e) A + e |ref| + floor, as in check_attention, with the floor of the
+    kernel that the call takes.  A weight enters as p vs / vref times a power of two, vref < 2 max vs being the power of
+    two at or above the largest value scale met so far:
+    * warp-MMA kernel: times 2^14 in fp16 planes whose last step is 2^-24, so a weight is off by up to 2^-25 of that,
+      2^-39 vref < 2^-38 max vs, times a code;
+    * tcgen05 kernel: times 2^9 in one plane (the running maximum may lag by 2^6), so up to 2^-34 vref < 2^-33 max vs;
+    for each of T weights, over a normaliser of at least 1; vref is not below 2^-126.  Beside it, results below fp32's
+    normal range are rounded to its step of 2^-149: half a step for each of at most T / 64 + 4 partials and the output."""
+    kc, ks, vc, vs = pools
+    q = [bt_.rows(bt_.qn, b) for b in range(len(bt_.lens))]
+    outs, mags, errs = q8.attend(q, kc, ks, vc, vs, bt_.table, bt_.lens, bt_.counts, bt_.bt, kind, scale)
+    fi = torch.finfo(DT[dtype])
+    e = fi.eps / 2 if dtype != "f32" else 0.0
+    step = 2.0 ** -33 if uses_tcgen05(dtype, bt_.counts, G) else 2.0 ** -38
+    got = got.double().cpu().numpy()
+    for b in range(len(bt_.lens)):
+        g = got[bt_.cu[b]:bt_.cu[b + 1]]
+        delta = (2.0 ** -22 + (bt_.d / 16 + 6) * 2.0 ** -23) * errs[b][..., None]
+        assert bt_.counts[b] == 0 or delta.max() <= 0.3
+        L = bt_.lens[b]
+        top = (127 if kind == "i8" else 448) * max(np.nanmax(vs.astype(np.float64)), 2.0 ** -127)
+        tol = (4 * delta + (L / 16 + 64) * 2.0 ** -23 + e) * mags[b] + e * np.abs(outs[b]) + step * L * top
+        tol += fi.eps * fi.tiny / 2 + (L / 64 + 4) * 2.0 ** -150
+        bad = ~(np.abs(g - outs[b]) <= tol)
+        assert not bad.any(), (b, int(bad.sum()), float(np.abs(g - outs[b])[bad].max()), float(tol[bad].max()))
+
+
+def attend(bt_, pools, kind="i8", scale=None, **kw):
+    one = max(bt_.counts) == 1 and min(bt_.counts) == 1
+    return ops.q8_attend_paged(bt_.q, *[cuda(p) for p in pools], bt_.t["table"], bt_.t["lens"], kind=kind,
+                               cu_q=None if one else bt_.t["cu"], max_q=None if one else max(bt_.counts), scale=scale, **kw)
+
+
+WARP_MMA = [f for f in FORMS if not uses_tcgen05(*f, 4)]
+
+
+# ---- value scales ----------------------------------------------------------------------------------------------------
+
+@pytest.mark.parametrize("dtype,counts", WARP_MMA)
+@pytest.mark.parametrize("tiny", [9.2e-41, 2.0 ** -126, 2.0 ** -114])
+def test_tiny_value_scales_before_ordinary_ones(dtype, counts, tiny):
+    """Blocks of zero values that a converted cache holds under a tiny scale, at the start of each sequence."""
+    bt_ = Batch(counts, [300, 150, 96], 8, 2, 128, 32, dtype, 301, pad=0)
+    pools = filled(bt_, "i8")
+    for b in range(3):
+        for t in range(0, 64, 16):
+            page = bt_.table[b, t // 32]
+            pools[2][page, :, t % 32:t % 32 + 16] = 0
+            pools[3][page, :, t % 32 // 16] = tiny
+    check(attend(bt_, pools), bt_, pools, "i8", 1 / math.sqrt(128), dtype, 4)
+
+
+@pytest.mark.parametrize("dtype,counts", [f for f in WARP_MMA if f[0] != "f16"])  # (fp16 holds no such outputs)
+@pytest.mark.parametrize("kind", ["i8", "e4m3"])
+@pytest.mark.parametrize("power", [-149, -140, -126, -114, 106])
+def test_value_scales_at_the_ends_of_fp32(dtype, counts, kind, power):
+    """Every value scale of one magnitude: 2^power to 2^(power + 4) (outputs below 2^-126 are subnormal)."""
+    bt_ = Batch(counts, [300, 150, 96], 8, 2, 128, 32, dtype, 302, pad=0)
+    pools = filled(bt_, kind)
+    vs = pools[3]
+    grow = 2.0 ** bt_.rng.integers(0, 5, vs.shape)
+    pools[3] = np.where(np.isnan(vs), vs, (2.0 ** power * grow).astype(np.float32)).astype(np.float32)
+    assert 2.0 ** (power + 4) * 448 * 300 < 2.0 ** 128  # sums over the cache stay within fp32
+    check(attend(bt_, pools, kind), bt_, pools, kind, 1 / math.sqrt(128), dtype, 4)
