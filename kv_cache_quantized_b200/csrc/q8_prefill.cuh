@@ -39,6 +39,7 @@ namespace axr {
 
 constexpr int kPfKeys = 128, kPfStep = 64, kPfThreads = 16 * 32;
 constexpr int kLazy = 6;
+constexpr float kNoScale = -150.f;  // lref before any positive value scale: below log2 of the smallest, 2^-149
 
 template <int D>
 struct PrefillPlan {
@@ -60,9 +61,9 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
-__device__ __forceinline__ float lg2(float x) {
+__device__ __forceinline__ float lg2(float x) {  // subnormal x included
   float y;
-  asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  asm("lg2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
 
@@ -307,7 +308,7 @@ q8_prefill_kernel(const __grid_constant__ Q8Attend a, const Q8Tiles tl) {
       ks = __ldg(a.kscales + next);
       vs = __ldg(a.vscales + next);
     }
-    float lref = -126.f;
+    float lref = kNoScale;
     for (int j = 0; j < n; ++j) {
       const int valid = end - begin - j * kPfKeys, st = j & 1;  // rows of the tile that some query sees
       const uint32_t ph = ((j >> 1) - 1) & 1;
@@ -400,7 +401,7 @@ q8_prefill_kernel(const __grid_constant__ Q8Attend a, const Q8Tiles tl) {
     const int q = warp >> 2;
     const uint32_t tq = tm + (static_cast<uint32_t>((warp & 3) * 32) << 16) + P::COL_S + 128 * q;
     const uint32_t to = tm + (static_cast<uint32_t>((warp & 3) * 32) << 16) + P::COL_O + 128 * q;
-    float m = threadIdx.x < nrow ? -INFINITY : 0.f, l = 0.f, lref = -126.f;  // rows not in use never ask for a second pass
+    float m = threadIdx.x < nrow ? -INFINITY : 0.f, l = 0.f, lref = kNoScale;  // rows not in use never ask for a second pass
     bool ok = true;
     // 16 columns of weights from 16 of S: 2^(s cc + off - m), packed to fp16; returns their sum
     auto weights = [&](const uint32_t (&x)[16], float cc, float off, uint32_t (&w)[8]) {
@@ -513,8 +514,9 @@ q8_prefill_kernel(const __grid_constant__ Q8Attend a, const Q8Tiles tl) {
     if (!ok) *failed = 1;
     const bool live = threadIdx.x < nrow;
     const float nan = __uint_as_float(0x7fc00000u);
-    const float unscale = ex2(lref - static_cast<float>(15 - kLazy));
-    const float f = a.splits == 1 ? (l == 0.f ? 0.f : unscale / l) : unscale;  // NaN stays
+    // times 2^lref in two factors (one could leave fp32's normal range), times 2^-(15 - kLazy), over l; NaN stays
+    const float half = floorf(0.5f * lref), f2 = ex2(lref - half);
+    const float f1 = ex2(half - static_cast<float>(15 - kLazy)) / (a.splits == 1 && l != 0.f ? l : 1.f);
     const int64_t part = ((tile * a.Hkv + hk) * kQ8PrefillRows + threadIdx.x) * a.splits + split;
 #pragma unroll 1
     for (int k = 0; k < D / 16; ++k) {
@@ -524,7 +526,7 @@ q8_prefill_kernel(const __grid_constant__ Q8Attend a, const Q8Tiles tl) {
         tc::ld_x16(to + 16 * k, o);
         tc::wait_ld();
 #pragma unroll
-        for (int e = 0; e < 16; ++e) x[e] = l == 0.f ? 0.f : __uint_as_float(o[e]) * f;
+        for (int e = 0; e < 16; ++e) x[e] = l == 0.f ? 0.f : __uint_as_float(o[e]) * f1 * f2;
       } else {
 #pragma unroll
         for (int e = 0; e < 16; ++e) x[e] = ok ? 0.f : nan;

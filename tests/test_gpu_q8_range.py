@@ -55,12 +55,9 @@ def attend(bt_, pools, kind="i8", scale=None, **kw):
                                cu_q=None if one else bt_.t["cu"], max_q=None if one else max(bt_.counts), scale=scale, **kw)
 
 
-WARP_MMA = [f for f in FORMS if not uses_tcgen05(*f, 4)]
-
-
 # ---- value scales ----------------------------------------------------------------------------------------------------
 
-@pytest.mark.parametrize("dtype,counts", WARP_MMA)
+@pytest.mark.parametrize("dtype,counts", FORMS)
 @pytest.mark.parametrize("tiny", [9.2e-41, 2.0 ** -126, 2.0 ** -114])
 def test_tiny_value_scales_before_ordinary_ones(dtype, counts, tiny):
     """Blocks of zero values that a converted cache holds under a tiny scale, at the start of each sequence."""
@@ -74,7 +71,7 @@ def test_tiny_value_scales_before_ordinary_ones(dtype, counts, tiny):
     check(attend(bt_, pools), bt_, pools, "i8", 1 / math.sqrt(128), dtype, 4)
 
 
-@pytest.mark.parametrize("dtype,counts", [f for f in WARP_MMA if f[0] != "f16"])  # (fp16 holds no such outputs)
+@pytest.mark.parametrize("dtype,counts", [f for f in FORMS if f[0] != "f16"])  # (fp16 holds no such outputs)
 @pytest.mark.parametrize("kind", ["i8", "e4m3"])
 @pytest.mark.parametrize("power", [-149, -140, -126, -114, 106])
 def test_value_scales_at_the_ends_of_fp32(dtype, counts, kind, power):
