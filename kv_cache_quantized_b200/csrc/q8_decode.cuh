@@ -319,7 +319,7 @@ q8_decode_kernel(const __grid_constant__ Q8Attend a, const __grid_constant__ Q8T
       // a power of two that brings the row's largest magnitude to [2^13, 2^14): the planes keep their precision
       int ex = 0;
       if (mx > 0.f && isfinite(mx)) frexpf(mx, &ex);
-      ex = max(-100, min(100, ex - 14));
+      ex = max(-120, min(114, ex - 14));  // 114: the largest finite queries; -120: 2^-ex stays well inside fp32's range
       const float up = ldexpf(1.f, -ex), fr = a.mult * ldexpf(1.f, ex);
 #pragma unroll
       for (int s = 0; s < KS; ++s)

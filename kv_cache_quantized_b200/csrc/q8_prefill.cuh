@@ -216,7 +216,7 @@ q8_prefill_kernel(const __grid_constant__ Q8Attend a, const Q8Tiles tl) {
     }
     int ex = 0;
     if (mx > 0.f && isfinite(mx)) frexpf(mx, &ex);
-    ex = max(-100, min(100, ex - 14));
+    ex = max(-120, min(114, ex - 14));  // 114: the largest finite queries; -120: 2^-ex stays well inside fp32's range
     const float up = ldexpf(a.mult < 0.f ? -1.f : 1.f, -ex);  // the operand carries the sign, so that f_row >= 0
     f_row = fabsf(a.mult) * ldexpf(1.f, ex);
     if (warp < 4 * nq) {

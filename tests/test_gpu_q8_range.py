@@ -1,4 +1,5 @@
-"""Attention over the 8-bit cache at the ends of what a call may hold: value scales from fp32's smallest to its largest."""
+"""Attention over the 8-bit cache at the ends of what a call may hold: value scales and queries from fp32's
+smallest magnitudes to its largest."""
 
 import math
 
@@ -83,3 +84,15 @@ def test_value_scales_at_the_ends_of_fp32(dtype, counts, kind, power):
     pools[3] = np.where(np.isnan(vs), vs, (2.0 ** power * grow).astype(np.float32)).astype(np.float32)
     assert 2.0 ** (power + 4) * 448 * 300 < 2.0 ** 128  # sums over the cache stay within fp32
     check(attend(bt_, pools, kind), bt_, pools, kind, 1 / math.sqrt(128), dtype, 4)
+
+
+# ---- queries ---------------------------------------------------------------------------------------------------------
+
+@pytest.mark.parametrize("dtype,counts", [f for f in FORMS if f[0] != "f16"])
+@pytest.mark.parametrize("power", [-120, -104, 104, 115, 118, 124])
+def test_queries_of_extreme_magnitude(dtype, counts, power):
+    """Finite queries far from one, key scales to match: the scores are ordinary."""
+    bt_ = Batch(counts, [300, 150, 96], 8, 2, 128, 32, dtype, 304, pad=0, scale=2.0 ** power)
+    pools = filled(bt_, "i8")
+    pools[1] = (pools[1] * np.float32(2.0 ** -power)).astype(np.float32)
+    check(attend(bt_, pools), bt_, pools, "i8", 1 / math.sqrt(128), dtype, 4)
