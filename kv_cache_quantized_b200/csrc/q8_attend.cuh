@@ -1,6 +1,6 @@
 // Attention over the paged 8-bit cache (q8.cuh): arguments and helpers shared by its kernels.
 //
-// Query row r = (token i, head g) of a sequence and KV head sees keys 0 .. pos0 + i, pos0 = len - count:
+// Query row r = (token i, head g) of a sequence and KV head sees keys 0 .. pos0 + i below T, pos0 = len - count:
 //   s_t = scale * ks_t (q . code^K_t),   o = sum_t 2^(s_t log2 e - m) vs_t code^V_t / sum_t 2^(s_t log2 e - m)
 // with ks_t, vs_t the scales of token t's 16-token block.
 #pragma once
@@ -30,15 +30,17 @@ struct Q8Attend {
   unsigned int* status;
 };
 
-// One sequence's query tokens and length.
+// One sequence's query tokens and length.  Positions come from the length as it is, the keys seen from that cut to T: a
+// length past T moves no token's causal limit.
 struct Q8Span {
-  int64_t first;  // first flat token
-  int count, pos0, len;
+  int64_t first;    // first flat token
+  int count, pos0;  // new tokens, position of the first
+  __device__ __forceinline__ int keys(int T) const { return min(pos0 + count, T); }
 };
 
 __device__ __forceinline__ Q8Span q8_span(const Q8Attend& a, int b) {
   Q8Span s;
-  const int len = a.seq_lens ? a.seq_lens[b] : a.T;
+  const int len = a.seq_lens ? max(a.seq_lens[b], 0) : a.T;
   int64_t lo = b, hi = static_cast<int64_t>(b) + 1;
   if (a.cu) {
     lo = a.cu[b];
@@ -47,8 +49,8 @@ __device__ __forceinline__ Q8Span q8_span(const Q8Attend& a, int b) {
   }
   s.first = lo;
   s.count = static_cast<int>(hi - lo);
-  s.len = max(0, min(len, a.T));
-  s.pos0 = s.len - s.count;
+  s.pos0 = len - s.count;
+  if (len > a.T && s.count > 0) atomicOr(a.status, kStatusBadIndex);
   return s;
 }
 
@@ -96,7 +98,7 @@ __device__ __forceinline__ Q8Span q8_tile_span(const Q8Attend& a, const Q8Tiles&
     i0 = 0;
     return q8_span(a, b);
   }
-  Q8Span r{0, 0, 0, 0};
+  Q8Span r{0, 0, 0};
   b = 0;
   i0 = -1;
 #pragma unroll 2
@@ -112,7 +114,6 @@ __device__ __forceinline__ Q8Span q8_tile_span(const Q8Attend& a, const Q8Tiles&
       r.first = __shfl_sync(0xffffffffu, s.first, src);
       r.count = __shfl_sync(0xffffffffu, s.count, src);
       r.pos0 = __shfl_sync(0xffffffffu, s.pos0, src);
-      r.len = __shfl_sync(0xffffffffu, s.len, src);
     }
   }
   return r;

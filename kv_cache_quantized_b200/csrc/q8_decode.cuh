@@ -79,10 +79,10 @@ struct Q8Extent {
   int rts;    // row tiles
   int tiles;  // key tiles of each (those of its last row tile)
 };
-__device__ __forceinline__ Q8Extent q8_extent(const Q8Tiles& tl, const Q8Span& sp) {
+__device__ __forceinline__ Q8Extent q8_extent(const Q8Attend& a, const Q8Tiles& tl, const Q8Span& sp) {
   Q8Extent e;
   e.rts = tl.one ? (sp.count > 0 && sp.count <= tl.tpt ? 1 : 0) : (sp.count + tl.tpt - 1) / tl.tpt;
-  e.tiles = e.rts > 0 ? (sp.len + kDecTile - 1) / kDecTile : 0;
+  e.tiles = e.rts > 0 ? (sp.keys(a.T) + kDecTile - 1) / kDecTile : 0;
   return e;
 }
 
@@ -106,7 +106,7 @@ struct Q8Flat {
                                               Q8Span& sp, Q8Extent& e, int64_t& ex, int64_t& n) {
     const bool on = b0 + lane < a.B;
     sp = q8_span(a, on ? b0 + lane : 0);
-    e = q8_extent(tl, sp);
+    e = q8_extent(a, tl, sp);
     n = on ? static_cast<int64_t>(e.rts) * a.Hkv * e.tiles : 0;
     int64_t inc = n;
 #pragma unroll
@@ -138,7 +138,6 @@ struct Q8Flat {
     r.sp.first = __shfl_sync(0xffffffffu, sp.first, src);
     r.sp.count = __shfl_sync(0xffffffffu, sp.count, src);
     r.sp.pos0 = __shfl_sync(0xffffffffu, sp.pos0, src);
-    r.sp.len = __shfl_sync(0xffffffffu, sp.len, src);
     r.ext.rts = __shfl_sync(0xffffffffu, e.rts, src);
     r.ext.tiles = __shfl_sync(0xffffffffu, e.tiles, src);
   }
@@ -171,7 +170,7 @@ struct Q8Flat {
     }
     r.b = 0;
     r.begin = 0;
-    r.sp = {0, 0, 0, 0};
+    r.sp = {0, 0, 0};
     r.ext = {0, 1};
     return r;
   }
@@ -243,7 +242,7 @@ q8_decode_kernel(const __grid_constant__ Q8Attend a, const __grid_constant__ Q8T
     x += k1 - k0;
     const int nrow = min(tl.tpt, sp.count - i0) * a.G;
     const int t_end = sp.pos0 + i0 + nrow / a.G;                  // keys the row tile's last token sees
-    const int end = min(k1 * kDecTile, t_end);
+    const int end = min(min(k1 * kDecTile, a.T), t_end);
     const int ntiles = failed ? 0 : max(0, (end + kDecTile - 1) / kDecTile - k0);
 
     // lane l: the pool's scale blocks (16 rows each) of key tile k0 + 32 i + l, -1 past the end, and their scales

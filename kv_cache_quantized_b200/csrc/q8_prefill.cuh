@@ -167,7 +167,7 @@ q8_prefill_kernel(const __grid_constant__ Q8Attend a, const Q8Tiles tl) {
   const int ntok = min(tl.tpt, sp.count - static_cast<int>(i0)), nrow = ntok * a.G;
   const int nq = nrow > 128 ? 2 : 1;                             // row tiles in use
   const int first_lim = sp.pos0 + static_cast<int>(i0) + 1;      // keys the tile's first token sees
-  const int begin = split * a.chunk, end = min(begin + a.chunk, first_lim + ntok - 1);
+  const int begin = split * a.chunk, end = min(min(begin + a.chunk, a.T), first_lim + ntok - 1);
   const int n = end > begin ? (end - begin + kPfKeys - 1) / kPfKeys : 0;  // operand stages
   const int ns = end > begin ? (end - begin + kPfStep - 1) / kPfStep : 0;  // steps
 

@@ -109,9 +109,10 @@ def append(x, codes, scales, table, lens, counts, bt, kind):
                 scales[page, h, off // BLOCK] = s
 
 
-def attend(q, kcodes, kscales, vcodes, vscales, table, lens, counts, bt, kind, scale):
-    """Causal attention in fp64.  q list per sequence of [count, Hq, d].  Returns lists of (out [count, Hq, d], the
-    magnitude sum_t p_t |v_t| of each output coordinate, the largest score error scale of each (token, head):
+def attend(q, kcodes, kscales, vcodes, vscales, table, lens, counts, bt, kind, scale, T=None):
+    """Causal attention in fp64.  q list per sequence of [count, Hq, d].  Keys at or past position T (None: no bound) are
+    seen by no token, whose own positions stay what they are.  Returns lists of (out [count, Hq, d], the magnitude
+    sum_t p_t |v_t| of each output coordinate, the largest score error scale of each (token, head):
     scale * max_t sum_j |q_j k_tj|)."""
     Hkv, d = kcodes.shape[1], kcodes.shape[3]
     outs, mags, errs = [], [], []
@@ -121,13 +122,14 @@ def attend(q, kcodes, kscales, vcodes, vscales, table, lens, counts, bt, kind, s
         G = Hq // Hkv
         o, mg, er = np.zeros((n, Hq, d)), np.zeros((n, Hq, d)), np.zeros((n, Hq))
         for h in range(Hkv):
-            k, v = np.zeros((L, d)), np.zeros((L, d))
-            for t in range(L):
+            keys = L if T is None else min(L, T)
+            k, v = np.zeros((keys, d)), np.zeros((keys, d))
+            for t in range(keys):
                 page, off = table[b][t // bt], t % bt
                 k[t] = values(kcodes[page, h, off], kind) * np.float64(kscales[page, h, off // BLOCK])
                 v[t] = values(vcodes[page, h, off], kind) * np.float64(vscales[page, h, off // BLOCK])
             for i in range(n):
-                last = L - n + i
+                last = min(L - n + i, keys - 1)
                 if last < 0:
                     continue
                 for g in range(G):

@@ -1,5 +1,5 @@
 """Attention over the 8-bit cache at the ends of what a call may hold: value scales and queries from fp32's
-smallest magnitudes to its largest."""
+smallest magnitudes to its largest, lengths past the caller's bound."""
 
 import math
 
@@ -7,7 +7,7 @@ import numpy as np
 import pytest
 import torch
 
-from kv_cache_quantized_b200 import ops
+from kv_cache_quantized_b200 import _abi, ops
 from oracle import q8
 from tests.test_gpu_q8 import DT, Batch, cuda, filled
 
@@ -22,7 +22,7 @@ def uses_tcgen05(dtype, counts, G):
     return dtype != "f32" and max(counts) * G > 16
 
 
-def check(got, bt_, pools, kind, scale, dtype, G):
+def check(got, bt_, pools, kind, scale, dtype, G, T=None):
     """|o - ref| <= (4 delta + (T / 16 + 64) 2^-23 + e) A + e |ref| + floor, as in check_attention, with the floor of the
     kernel that the call takes.  A weight enters as p vs / vref times a power of two, vref < 2 max vs being the power of
     two at or above the largest value scale met so far:
@@ -33,7 +33,7 @@ def check(got, bt_, pools, kind, scale, dtype, G):
     normal range are rounded to its step of 2^-149: half a step for each of at most T / 64 + 4 partials and the output."""
     kc, ks, vc, vs = pools
     q = [bt_.rows(bt_.qn, b) for b in range(len(bt_.lens))]
-    outs, mags, errs = q8.attend(q, kc, ks, vc, vs, bt_.table, bt_.lens, bt_.counts, bt_.bt, kind, scale)
+    outs, mags, errs = q8.attend(q, kc, ks, vc, vs, bt_.table, bt_.lens, bt_.counts, bt_.bt, kind, scale, T)
     fi = torch.finfo(DT[dtype])
     e = fi.eps / 2 if dtype != "f32" else 0.0
     step = 2.0 ** -33 if uses_tcgen05(dtype, bt_.counts, G) else 2.0 ** -38
@@ -96,3 +96,20 @@ def test_queries_of_extreme_magnitude(dtype, counts, power):
     pools = filled(bt_, "i8")
     pools[1] = (pools[1] * np.float32(2.0 ** -power)).astype(np.float32)
     check(attend(bt_, pools), bt_, pools, "i8", 1 / math.sqrt(128), dtype, 4)
+
+
+# ---- lengths and offsets out of range --------------------------------------------------------------------------------
+
+@pytest.mark.parametrize("dtype,counts", FORMS)
+@pytest.mark.parametrize("T", [256, 100, 37])
+def test_lengths_past_the_bound_keep_their_positions(dtype, counts, T):
+    """Keys at or past T are not seen; a token's causal limit stays its own position; the call is flagged."""
+    bt_ = Batch(counts, [300, 150, 96], 8, 2, 128, 32, dtype, 305, pad=0)
+    pools = filled(bt_, "i8")
+    ops.device_status(clear=True)
+    got = attend(bt_, pools, T=T)
+    assert ops.device_status(clear=True) == _abi.STATUS_BAD_INDEX
+    check(got, bt_, pools, "i8", 1 / math.sqrt(128), dtype, 4, T)
+    got = attend(bt_, pools, T=300)
+    assert ops.device_status() == 0
+    check(got, bt_, pools, "i8", 1 / math.sqrt(128), dtype, 4)
