@@ -59,10 +59,13 @@ __device__ __forceinline__ NewSpan find_span(const PagedNew& p, int64_t key, int
   int lo = 0, hi = 0, len = 0;
   if (p.cu) {
     b = 0;
+    const unsigned n_tok = static_cast<unsigned>(p.n_tok);
+    bool bad = false;
 #pragma unroll 2
     for (int b0 = 0; b0 < p.B; b0 += 32) {
       const int c = min(b0 + lane, p.B - 1);
       const int l = p.cu[c], h = p.cu[c + 1], n = p.seq_lens[c];
+      bad |= static_cast<unsigned>(l) > static_cast<unsigned>(h) || static_cast<unsigned>(h) > n_tok;  // negative ones too
       const unsigned who = __ballot_sync(0xffffffffu, b0 + lane < p.B && first(l, c) <= key);
       if (who || b0 == 0) {
         const int src = who ? 31 - __clz(who) : 0;
@@ -73,6 +76,7 @@ __device__ __forceinline__ NewSpan find_span(const PagedNew& p, int64_t key, int
       }
     }
     if (lo < 0 || hi > p.n_tok || hi < lo) lo = hi = 0;  // an inconsistent table has no new tokens here
+    if (bad) atomicOr(p.status, kStatusBadIndex);
   } else {
     b = static_cast<int>(key);
     lo = b;

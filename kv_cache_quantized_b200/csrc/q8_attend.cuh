@@ -42,15 +42,19 @@ __device__ __forceinline__ Q8Span q8_span(const Q8Attend& a, int b) {
   Q8Span s;
   const int len = a.seq_lens ? max(a.seq_lens[b], 0) : a.T;
   int64_t lo = b, hi = static_cast<int64_t>(b) + 1;
+  bool bad = false;
   if (a.cu) {
     lo = a.cu[b];
     hi = a.cu[b + 1];
-    if (lo < 0 || hi > a.n_tok || hi < lo) lo = hi = 0;
+    if (lo < 0 || hi > a.n_tok || hi < lo) {  // no sequence of this batch: it counts as empty
+      lo = hi = 0;
+      bad = true;
+    }
   }
   s.first = lo;
   s.count = static_cast<int>(hi - lo);
   s.pos0 = len - s.count;
-  if (len > a.T && s.count > 0) atomicOr(a.status, kStatusBadIndex);
+  if (bad || (len > a.T && s.count > 0)) atomicOr(a.status, kStatusBadIndex);
   return s;
 }
 

@@ -1,5 +1,5 @@
-"""Attention over the 8-bit cache at the ends of what a call may hold: value scales and queries from fp32's
-smallest magnitudes to its largest, lengths past the caller's bound."""
+"""Attention over the 8-bit cache and the paged appends at the ends of what a call may hold: value scales and queries from
+fp32's smallest magnitudes to its largest, lengths and offsets out of range."""
 
 import math
 
@@ -113,3 +113,24 @@ def test_lengths_past_the_bound_keep_their_positions(dtype, counts, T):
     got = attend(bt_, pools, T=300)
     assert ops.device_status() == 0
     check(got, bt_, pools, "i8", 1 / math.sqrt(128), dtype, 4)
+
+
+@pytest.mark.parametrize("dtype,max_q", [("f32", None), ("bf16", None), ("bf16", 3), ("f16", 64)])
+@pytest.mark.parametrize("cu", [[0, 5, 3, 8], [0, 3, 6, 99], [-2, 3, 6, 8]])
+def test_offsets_that_make_no_sense_are_flagged(dtype, max_q, cu):
+    """Decreasing, negative or too large offsets: their sequence counts as empty, and the call is flagged, by the attention
+    and by both appends, while every other sequence whose tokens are its own is served."""
+    good = Batch([3, 3, 2], [40, 50, 60], 8, 2, 128, 32, dtype, 307, pad=0)
+    pools = filled(good, "i8")
+    bad = cuda(np.array(cu, np.int32))
+    dev = [cuda(p) for p in pools]
+    ops.device_status(clear=True)
+    ops.q8_attend_paged(good.q, *dev, good.t["table"], good.t["lens"], cu_q=bad, max_q=max_q)
+    assert ops.device_status(clear=True) & _abi.STATUS_BAD_INDEX
+    ops.q8_append_paged(good.k, good.v, *dev, good.t["table"], good.t["lens"], cu_new=bad)
+    assert ops.device_status(clear=True) & _abi.STATUS_BAD_INDEX
+    z = lambda *sh, dt: torch.zeros(sh, dtype=dt, device="cuda")
+    ops.append_paged(good.k, good.v, z(good.nb, 2, 32, 64, dt=torch.uint8), z(good.nb, 2, 32, dt=torch.float16),
+                     torch.ones(128, dtype=torch.int8, device="cuda"), 4, good.t["table"], good.t["lens"], cu_new=bad,
+                     v=z(good.nb, 2, 32, 128, dt=torch.float16))
+    assert ops.device_status(clear=True) & _abi.STATUS_BAD_INDEX
