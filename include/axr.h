@@ -393,9 +393,9 @@ AXR_API axr_status axr_pot_attend_decode(const float* q, const uint8_t* codes, c
  *   positions    [dev] [n_tok] int32 rotation positions, or NULL: the cache positions;
  *   q_out        [dev] out, the rotated queries, contiguous; NULL together with q.
  * Tokens whose cache position is negative are skipped.  Tokens past the block table's reach, with a table entry outside
- * [0, num_blocks) or a rotation position outside [0, max_pos) are skipped and set AXR_STATUS_BAD_INDEX.  So do entries
- * of cu that decrease or leave [0, n_tok], whose sequence counts as empty (its rows of q_out and out stay as they are).
- * No two
+ * [0, num_blocks) or a rotation position outside [0, max_pos) are skipped and set AXR_STATUS_BAD_INDEX.  So do a
+ * negative length, which counts as 0, and entries of cu that decrease or leave [0, n_tok], whose sequence counts as
+ * empty (its rows of q_out and out stay as they are).  No two
  * sequences may have new tokens in one pool block, nor may a block that another sequence reads get new tokens (its older
  * codes may be rounded again; copy it first).  Inputs must be finite: in the 8-bit cache NaN is held as 0 and an
  * infinity as the block's largest code (neither counts towards its scale).

@@ -83,6 +83,10 @@ __device__ __forceinline__ NewSpan find_span(const PagedNew& p, int64_t key, int
     hi = b + 1;
     len = p.seq_lens[b];
   }
+  if (len < 0) {
+    if (hi > lo && lane == 0) atomicOr(p.status, kStatusBadIndex);
+    len = 0;
+  }
   s.first = lo;
   s.count = hi - lo;
   s.pos0 = len - s.count;

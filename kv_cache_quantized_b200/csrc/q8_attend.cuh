@@ -40,7 +40,7 @@ struct Q8Span {
 
 __device__ __forceinline__ Q8Span q8_span(const Q8Attend& a, int b) {
   Q8Span s;
-  const int len = a.seq_lens ? max(a.seq_lens[b], 0) : a.T;
+  const int len = a.seq_lens ? a.seq_lens[b] : a.T;
   int64_t lo = b, hi = static_cast<int64_t>(b) + 1;
   bool bad = false;
   if (a.cu) {
@@ -53,8 +53,8 @@ __device__ __forceinline__ Q8Span q8_span(const Q8Attend& a, int b) {
   }
   s.first = lo;
   s.count = static_cast<int>(hi - lo);
-  s.pos0 = len - s.count;
-  if (bad || (len > a.T && s.count > 0)) atomicOr(a.status, kStatusBadIndex);
+  s.pos0 = max(len, 0) - s.count;
+  if (bad || (s.count > 0 && (len < 0 || len > a.T))) atomicOr(a.status, kStatusBadIndex);
   return s;
 }
 

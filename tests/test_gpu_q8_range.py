@@ -9,7 +9,7 @@ import torch
 
 from kv_cache_quantized_b200 import _abi, ops
 from oracle import q8
-from tests.test_gpu_q8 import DT, Batch, cuda, filled
+from tests.test_gpu_q8 import DT, Batch, cuda, filled, rope_table, same
 
 pytestmark = pytest.mark.gpu
 
@@ -115,6 +115,19 @@ def test_lengths_past_the_bound_keep_their_positions(dtype, counts, T):
     check(got, bt_, pools, "i8", 1 / math.sqrt(128), dtype, 4)
 
 
+@pytest.mark.parametrize("dtype,counts", FORMS)
+def test_a_negative_length_is_flagged_and_counts_as_none(dtype, counts):
+    bt_ = Batch(counts, [300, 150, 96], 8, 2, 128, 32, dtype, 306, pad=0)
+    pools = filled(bt_, "i8")
+    bt_.t["lens"][1] = -7
+    bt_.lens = [300, 0, 96]
+    ops.device_status(clear=True)
+    got = attend(bt_, pools)
+    assert ops.device_status(clear=True) == _abi.STATUS_BAD_INDEX
+    assert torch.all(got[int(bt_.cu[1]):int(bt_.cu[2])] == 0)
+    check(got, bt_, pools, "i8", 1 / math.sqrt(128), dtype, 4)
+
+
 @pytest.mark.parametrize("dtype,max_q", [("f32", None), ("bf16", None), ("bf16", 3), ("f16", 64)])
 @pytest.mark.parametrize("cu", [[0, 5, 3, 8], [0, 3, 6, 99], [-2, 3, 6, 8]])
 def test_offsets_that_make_no_sense_are_flagged(dtype, max_q, cu):
@@ -134,3 +147,23 @@ def test_offsets_that_make_no_sense_are_flagged(dtype, max_q, cu):
                      torch.ones(128, dtype=torch.int8, device="cuda"), 4, good.t["table"], good.t["lens"], cu_new=bad,
                      v=z(good.nb, 2, 32, 128, dt=torch.float16))
     assert ops.device_status(clear=True) & _abi.STATUS_BAD_INDEX
+
+
+def test_a_negative_length_is_flagged_by_the_appends():
+    bt_ = Batch([3, 3, 2], [40, 50, 60], 8, 2, 128, 32, "f16", 308, pad=0)
+    pools = filled(bt_, "i8")
+    dev = [cuda(p) for p in pools]
+    bt_.t["lens"][:] = torch.tensor([-1, -40, -2 ** 31])
+    before = [p.clone() for p in dev]
+    qo = torch.full((8, 8, 128), 3.0, dtype=torch.float16, device="cuda")
+    ops.device_status(clear=True)
+    ops.q8_append_paged(bt_.k, bt_.v, *dev, bt_.t["table"], bt_.t["lens"], cu_new=bt_.t["cu"], q=bt_.q, q_out=qo,
+                        cos_sin=cuda(rope_table(64, 128)))
+    assert ops.device_status(clear=True) == _abi.STATUS_BAD_INDEX
+    assert same(dev, before) and torch.all(qo == 3)
+    kc, kn = torch.full((bt_.nb, 2, 32, 64), 9, dtype=torch.uint8, device="cuda"), torch.ones((bt_.nb, 2, 32), device="cuda").half()
+    v = torch.ones((bt_.nb, 2, 32, 128), device="cuda").half()
+    ops.append_paged(bt_.k, bt_.v, kc, kn, torch.ones(128, dtype=torch.int8, device="cuda"), 4, bt_.t["table"],
+                     bt_.t["lens"], cu_new=bt_.t["cu"], v=v)
+    assert ops.device_status(clear=True) == _abi.STATUS_BAD_INDEX
+    assert torch.all(kc == 9) and torch.all(kn == 1) and torch.all(v == 1)
