@@ -38,24 +38,25 @@ struct Q8Span {
   __device__ __forceinline__ int keys(int T) const { return min(pos0 + count, T); }
 };
 
-__device__ __forceinline__ Q8Span q8_span(const Q8Attend& a, int b) {
+// From the entries cu[b], cu[b + 1] and the length.  Entries that make no sense, or a length out of range, set the status
+// word; a sequence of such entries counts as empty.
+__device__ __forceinline__ Q8Span q8_span_of(const Q8Attend& a, int64_t lo, int64_t hi, int len) {
   Q8Span s;
-  const int len = a.seq_lens ? a.seq_lens[b] : a.T;
-  int64_t lo = b, hi = static_cast<int64_t>(b) + 1;
   bool bad = false;
-  if (a.cu) {
-    lo = a.cu[b];
-    hi = a.cu[b + 1];
-    if (lo < 0 || hi > a.n_tok || hi < lo) {  // no sequence of this batch: it counts as empty
-      lo = hi = 0;
-      bad = true;
-    }
+  if (lo < 0 || hi > a.n_tok || hi < lo) {
+    lo = hi = 0;
+    bad = true;
   }
   s.first = lo;
   s.count = static_cast<int>(hi - lo);
   s.pos0 = max(len, 0) - s.count;
   if (bad || (s.count > 0 && (len < 0 || len > a.T))) atomicOr(a.status, kStatusBadIndex);
   return s;
+}
+
+__device__ __forceinline__ Q8Span q8_span(const Q8Attend& a, int b) {
+  const int len = a.seq_lens ? a.seq_lens[b] : a.T;
+  return a.cu ? q8_span_of(a, a.cu[b], a.cu[b + 1], len) : q8_span_of(a, b, static_cast<int64_t>(b) + 1, len);
 }
 
 // How a kernel cuts the query tokens into row tiles of up to tpt tokens (times the heads of a group).
@@ -102,25 +103,30 @@ __device__ __forceinline__ Q8Span q8_tile_span(const Q8Attend& a, const Q8Tiles&
     i0 = 0;
     return q8_span(a, b);
   }
-  Q8Span r{0, 0, 0};
+  const unsigned n_tok = static_cast<unsigned>(a.n_tok);
+  int lo = 0, hi = 0, len = 0;
+  bool bad = false;
   b = 0;
   i0 = -1;
 #pragma unroll 2
   for (int b0 = 0; b0 < a.B; b0 += 32) {
     const int c = min(b0 + lane, a.B - 1);
-    const Q8Span s = q8_span(a, c);
-    const int64_t first = static_cast<int64_t>(a.cu[c] / tl.tpt) + c;
+    const int l = a.cu[c], h = a.cu[c + 1], n = a.seq_lens ? a.seq_lens[c] : a.T;
+    // every sequence's offsets (as unsigned, negative ones are large); lengths where a tile has them
+    bad |= static_cast<unsigned>(l) > static_cast<unsigned>(h) || static_cast<unsigned>(h) > n_tok;
+    const int64_t first = static_cast<int64_t>(l / tl.tpt) + c;
     const unsigned who = __ballot_sync(0xffffffffu, b0 + lane < a.B && first <= tile);
     if (who) {
       const int src = 31 - __clz(who);
       b = b0 + src;
       i0 = (tile - __shfl_sync(0xffffffffu, first, src)) * tl.tpt;
-      r.first = __shfl_sync(0xffffffffu, s.first, src);
-      r.count = __shfl_sync(0xffffffffu, s.count, src);
-      r.pos0 = __shfl_sync(0xffffffffu, s.pos0, src);
+      lo = __shfl_sync(0xffffffffu, l, src);
+      hi = __shfl_sync(0xffffffffu, h, src);
+      len = __shfl_sync(0xffffffffu, n, src);
     }
   }
-  return r;
+  if (bad) atomicOr(a.status, kStatusBadIndex);
+  return q8_span_of(a, lo, hi, len);
 }
 
 __device__ __forceinline__ bool q8_tile_live(const Q8Attend& a, const Q8Tiles& tl, const Q8Span& sp, int64_t i0,

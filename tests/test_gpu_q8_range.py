@@ -129,7 +129,7 @@ def test_a_negative_length_is_flagged_and_counts_as_none(dtype, counts):
 
 
 @pytest.mark.parametrize("dtype,max_q", [("f32", None), ("bf16", None), ("bf16", 3), ("f16", 64)])
-@pytest.mark.parametrize("cu", [[0, 5, 3, 8], [0, 3, 6, 99], [-2, 3, 6, 8]])
+@pytest.mark.parametrize("cu", [[0, 5, 3, 8], [0, 3, 6, 99], [-2, 3, 6, 8], [90, 91, 92, 93]])
 def test_offsets_that_make_no_sense_are_flagged(dtype, max_q, cu):
     """Decreasing, negative or too large offsets: their sequence counts as empty, and the call is flagged, by the attention
     and by both appends, while every other sequence whose tokens are its own is served."""
