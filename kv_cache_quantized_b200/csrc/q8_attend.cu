@@ -46,13 +46,19 @@ Q8Plan plan_decode(int64_t n_tok, int B, int G, int Hkv, int T, bool one, int ma
   return pl;
 }
 
+constexpr int64_t kMaxPartials = 16 * kSmCount * kQ8PrefillRows;  // 315 MB of workspace at d = 128
+
 // The tcgen05 kernel: tiles of 256 rows, one thread block per SM, a tile a sequence where max_q allows it.  In units of
 // one key tile (128 tokens), a block's set-up (query operand, first code tiles) costs about 2, and writing and merging
 // the partials of a split axis up to 3 more: a full tile's 256 x d fp32 rows cross HBM twice.  The host knows no
 // lengths: how many tiles have work is estimated, with every sequence, or, beside a launch for those of up to `few`
 // tokens, as many longer ones as there must be.  (A count of the numbered tiles instead of those with work split 148
-// units of 64 key tiles in four: 173 against 117 us.)  The workspace holds partials for every numbered tile, with work
-// or without, so a split stops at 16 blocks an SM: 315 MB at d = 128.
+// units of 64 key tiles in four: 173 against 117 us.)  The workspace holds a partial for each query row and split, and a
+// split stops at kMaxPartials of them.  (A bound on the numbered tiles, with work or without, left a chunk of 64 tokens
+// on 32768 keys beside 199 single tokens in one piece: 751 against 450 us.)
+// Beside short sequences most blocks have no work: they cost about one unit a wave of SMs and split, and from 9 splits on,
+// where the merge takes a block a row, 0.65 for 16 such blocks an SM (59 single tokens and the chunk: 8 splits 184 us, 10
+// splits 251 us; 15 single tokens: 16 splits 112 us, 8 splits 120 us).
 Q8Plan plan_prefill(int64_t n_tok, int B, int G, int Hkv, int T, int max_q, int few) {
   Q8Plan pl;
   pl.nrg = kQ8PrefillRows / 8;
@@ -68,14 +74,15 @@ Q8Plan plan_prefill(int64_t n_tok, int B, int G, int Hkv, int T, int max_q, int 
   const int64_t units = live * Hkv, total = (static_cast<int64_t>(T) + 127) / 128;
   const double fill = std::min(1.0, static_cast<double>(n_tok) * G / (static_cast<double>(live) * kQ8PrefillRows));
   const auto waves = [&](int64_t s) { return static_cast<double>((units * s + kSmCount - 1) / kSmCount); };
-  // blocks without work take about 0.7 a wave
-  const double idle = 0.7 * static_cast<double>(pl.tl.tiles * Hkv - units) / kSmCount;
+  const double idle = static_cast<double>(pl.tl.tiles * Hkv - units) / kSmCount;
+  const double idle_rows = 0.65 / 16 * idle * std::min(max_q, pl.tl.tpt) * G;
   pl.sp.splits = 1;
   pl.sp.chunk = static_cast<int>(total * 128);
   double best = waves(1) * (total + 2) + idle;
-  for (int64_t s = 2; s <= total / 2 && s <= 256 && pl.tl.tiles * Hkv * s <= 16 * kSmCount; ++s) {
+  const int64_t rows = n_tok * G * Hkv;
+  for (int64_t s = 2; s <= total / 2 && s <= 256 && rows * s <= kMaxPartials; ++s) {
     const int64_t per = (total + s - 1) / s, splits = (total + per - 1) / per;
-    const double cost = waves(splits) * (per + 2 + 3 * fill) + idle * splits;
+    const double cost = waves(splits) * (per + 2 + 3 * fill) + idle * splits + (splits > 8 ? idle_rows : 0.0);
     if (cost < best) {
       best = cost;
       pl.sp.splits = static_cast<int>(splits);
@@ -83,7 +90,7 @@ Q8Plan plan_prefill(int64_t n_tok, int B, int G, int Hkv, int T, int max_q, int 
     }
   }
   pl.grid = 0;
-  pl.parts = pl.sp.splits == 1 ? 0 : static_cast<size_t>(pl.tl.tiles) * Hkv * kQ8PrefillRows * pl.sp.splits;
+  pl.parts = pl.sp.splits == 1 ? 0 : static_cast<size_t>(rows) * pl.sp.splits;
   return pl;
 }
 

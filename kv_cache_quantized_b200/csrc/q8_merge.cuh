@@ -108,9 +108,8 @@ q8_merge_kernel(const __grid_constant__ Q8Attend a, const __grid_constant__ Q8Ti
   wait();  // the partials are complete and visible after this
   const int end = min(nrow, min(rows, r0 + per));
   for (int r = r0 + (NW == 1 ? static_cast<int>(threadIdx.x) >> 5 : 0); r < end; r += kMergeWarps) {
-    const int64_t p0 = (static_cast<int64_t>(unit) * kQ8PrefillRows + r) * a.splits;
     const int64_t orow = (sp.first + i0 + r / a.G) * a.Hq + static_cast<int64_t>(hk) * a.G + r % a.G;
-    q8_merge_row<T, D, NW>(a, a.splits, [&](int k) { return p0 + k; }, orow);
+    q8_merge_row<T, D, NW>(a, a.splits, [&](int k) { return orow * a.splits + k; }, orow);
   }
 }
 

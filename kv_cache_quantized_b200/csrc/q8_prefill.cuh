@@ -517,7 +517,7 @@ q8_prefill_kernel(const __grid_constant__ Q8Attend a, const Q8Tiles tl) {
     // times 2^lref in two factors (one could leave fp32's normal range), times 2^-(15 - kLazy), over l; NaN stays
     const float half = floorf(0.5f * lref), f2 = ex2(lref - half);
     const float f1 = ex2(half - static_cast<float>(15 - kLazy)) / (a.splits == 1 && l != 0.f ? l : 1.f);
-    const int64_t part = ((tile * a.Hkv + hk) * kQ8PrefillRows + threadIdx.x) * a.splits + split;
+    const int64_t part = orow * a.splits + split;
 #pragma unroll 1
     for (int k = 0; k < D / 16; ++k) {
       uint32_t o[16];

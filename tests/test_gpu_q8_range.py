@@ -1,5 +1,6 @@
 """Attention over the 8-bit cache and the paged appends at the ends of what a call may hold: value scales and queries from
-fp32's smallest magnitudes to its largest, lengths and offsets out of range."""
+fp32's smallest magnitudes to its largest, lengths and offsets out of range, a split of the token axis beside many single
+tokens."""
 
 import math
 
@@ -167,3 +168,27 @@ def test_a_negative_length_is_flagged_by_the_appends():
                      bt_.t["lens"], cu_new=bt_.t["cu"], v=v)
     assert ops.device_status(clear=True) == _abi.STATUS_BAD_INDEX
     assert torch.all(kc == 9) and torch.all(kn == 1) and torch.all(v == 1)
+
+
+# ---- a split axis beside many single tokens --------------------------------------------------------------------------
+
+@pytest.mark.parametrize("dtype,kind", [("bf16", "i8"), ("f16", "e4m3")])
+def test_a_chunk_on_a_long_axis_beside_many_single_tokens(dtype, kind):
+    """A chunk whose token axis is split, among more numbered tiles than SMs; the workspace is of the size asked for, and
+    what lies behind it stays as it was."""
+    counts = [1] * 100 + [64] + [1] * 99
+    lens = [1 + 7 * i % 90 for i in range(100)] + [4100] + [1 + 5 * i % 60 for i in range(99)]
+    bt_ = Batch(counts, lens, 16, 8, 64, 64, dtype, 310)
+    pools = filled(bt_, kind)
+    T = 16384  # a bound that a server with long sequences would give
+    table = np.full((200, T // 64), -7, np.int32)
+    table[:, :bt_.mb] = bt_.table
+    need = ops.q8_attend_workspace_bytes(bt_.n_tok, 64, 200, 16, 8, T, 64)
+    ws = torch.full((need + 4096,), 77, dtype=torch.uint8, device="cuda")
+    out = torch.full((bt_.n_tok, 16, 64), 55.0, dtype=DT[dtype], device="cuda")
+    ops.device_status(clear=True)
+    ops.q8_attend_paged(bt_.q, *[cuda(p) for p in pools], cuda(table), bt_.t["lens"], kind=kind, cu_q=bt_.t["cu"], max_q=64,
+                        T=T, out=out, workspace=ws[:need])
+    assert ops.device_status() == 0
+    assert torch.all(ws[need:] == 77) and torch.all(out[int(bt_.cu[-1]):] == 55.0)
+    check(out, bt_, pools, kind, 1 / math.sqrt(64), dtype, 2)
