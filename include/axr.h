@@ -421,10 +421,14 @@ AXR_API axr_status axr_pot_attend_decode(const float* q, const uint8_t* codes, c
  *   sequence b sees the cache positions up to its own.  out [n_tok, Hq, d] of x_dtype.  Sums and softmax statistics
  *   are fp32, codes enter the tensor cores exactly.  fp32 queries and weights enter as hi and lo fp16 planes (about 22
  *   bits), 16-bit ones as one fp16 plane (2^-11 a weight); calls of up to 16 query rows (tokens x heads of a group) a
- *   sequence, and short sequences among long ones, keep two planes for the weights of fp16 calls.  Queries and scales may
- *   have any finite magnitude (query coordinates are held to within 2^-145, subnormal value scales as they are) as long as
- *   scale q, the products of a score and the sum of a sequence's values stay within fp32's range.  A token that sees
- *   nothing (seq_lens[b] smaller than its sequence's token count) gets 0.
+ *   sequence, and short sequences among long ones, keep two planes for the weights of fp16 calls.  A weight carries its
+ *   token's value scale, relative to the largest met so far, and fp16's smallest step is its floor: a token's value is
+ *   held to within 2^-38 of the largest value scale times its code in those calls and in fp32, to within 2^-33 elsewhere
+ *   (more than 16 rows of 16-bit queries), which shows where a row's weight lies on blocks whose scale is 2^-23 or less
+ *   of another visible block's.  Queries and scales may have any finite magnitude (query coordinates are held to within
+ *   2^-145, subnormal value scales as they are) as long as scale q, the products of a score and the sum of a sequence's
+ *   values stay within fp32's range.  A token that sees nothing (seq_lens[b] smaller than its sequence's token count)
+ *   gets 0.
  *   max_q an upper bound of a sequence's query tokens, or 0 if unknown (a tight one picks the better kernel); rows of a
  *   sequence with more may stay unwritten, which sets AXR_STATUS_BAD_INDEX.  T an upper bound of the lengths; seq_lens
  *   NULL: all T.  A longer sequence's tokens keep their positions, but see no key at or past T, which sets

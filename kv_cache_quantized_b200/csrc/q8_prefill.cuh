@@ -18,7 +18,8 @@
 // ahead into registers and turn them into fp16 operands, two tiles deep, once for both row tiles; warps 12..15 issue
 // the MMAs of S and of O, one product of one row tile each.
 //
-// Roundings: the weights to fp16 (2^-11; the output is 16-bit), bf16 queries to fp16 after a power of two brought their
+// Roundings: the weights to fp16 (2^-11; the output is 16-bit; no finer than 2^-33 of the largest value scale, half of
+// fp16's last step below 2^(15 - kLazy)), bf16 queries to fp16 after a power of two brought their
 // row's largest magnitude to 2^13..2^14 (exact for coordinates within 2^-27 of it).  The running maximum moves only
 // when it grows by more than 2^kLazy (weights stay below 2^kLazy, and inside fp16 with the 2^(15 - kLazy) they are
 // scaled by), so the output is seldom rescaled, and a tile takes one pass over S: the weights are formed with the

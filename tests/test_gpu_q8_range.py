@@ -87,6 +87,22 @@ def test_value_scales_at_the_ends_of_fp32(dtype, counts, kind, power):
     check(attend(bt_, pools, kind), bt_, pools, kind, 1 / math.sqrt(128), dtype, 4)
 
 
+@pytest.mark.parametrize("dtype,counts", FORMS)
+def test_attention_on_blocks_of_small_value_scale(dtype, counts):
+    """Rows whose weight lies on blocks with value scales 2^-20 to 2^-26 of another visible block's: held to the floors
+    that the kernels state, 2^-38 or 2^-33 of the largest scale."""
+    bt_ = Batch(counts, [300, 150, 96], 8, 2, 128, 32, dtype, 303, pad=0)
+    pools = filled(bt_, "i8")
+    kc, ks, vc, vs = pools
+    for b in range(3):  # the first block keeps its scale and one value; all other coordinates come from small blocks
+        page = bt_.table[b, 0]
+        vc[page, :, :16] = 0
+        vc[page, :, 0, 0] = 127
+        for t in range(16, bt_.lens[b], 16):
+            vs[bt_.table[b, t // 32], :, t % 32 // 16] *= np.float32(2.0 ** -bt_.rng.integers(20, 27))
+    check(attend(bt_, pools), bt_, pools, "i8", 1 / math.sqrt(128), dtype, 4)
+
+
 # ---- queries ---------------------------------------------------------------------------------------------------------
 
 @pytest.mark.parametrize("dtype,counts", [f for f in FORMS if f[0] != "f16"])
