@@ -186,6 +186,27 @@ def test_a_negative_length_is_flagged_by_the_appends():
     assert torch.all(kc == 9) and torch.all(kn == 1) and torch.all(v == 1)
 
 
+# ---- one sequence, alone and among others ----------------------------------------------------------------------------
+
+@pytest.mark.parametrize("dtype,counts", FORMS)
+def test_a_sequence_alone_and_among_others(dtype, counts):
+    """The other sequences of a batch decide where the token axis is cut, so the bits may differ; both results lie within
+    the bound, and the same call gives the same bits."""
+    bt_ = Batch(counts, [900, 333, 64], 8, 2, 128, 32, dtype, 309, pad=0)
+    pools = filled(bt_, "i8")
+    a, b = attend(bt_, pools), attend(bt_, pools)
+    assert torch.equal(a, b)
+    check(a, bt_, pools, "i8", 1 / math.sqrt(128), dtype, 4)
+    dev = [cuda(p) for p in pools]
+    alone = []
+    for s in range(3):
+        lo, hi = int(bt_.cu[s]), int(bt_.cu[s + 1])
+        cu = cuda(np.array([0, hi - lo], np.int32))
+        alone.append(ops.q8_attend_paged(bt_.q[lo:hi], *dev, bt_.t["table"][s:s + 1], bt_.t["lens"][s:s + 1],
+                                         cu_q=None if max(counts) == 1 else cu, max_q=hi - lo))
+    check(torch.cat(alone), bt_, pools, "i8", 1 / math.sqrt(128), dtype, 4)
+
+
 # ---- a split axis beside many single tokens --------------------------------------------------------------------------
 
 @pytest.mark.parametrize("dtype,kind", [("bf16", "i8"), ("f16", "e4m3")])
