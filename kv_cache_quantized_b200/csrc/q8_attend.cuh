@@ -149,14 +149,12 @@ __device__ __forceinline__ int64_t q8_row(const Q8Attend& a, int b, int hk, int 
   return ((static_cast<int64_t>(page) * a.Hkv + hk) << a.shift) + (t & ((1 << a.shift) - 1));
 }
 
-template <typename T>
-__device__ __forceinline__ float to_float(T x);
-template <>
-__device__ __forceinline__ float to_float<float>(float x) { return x; }
-template <>
-__device__ __forceinline__ float to_float<__half>(__half x) { return __half2float(x); }
-template <>
-__device__ __forceinline__ float to_float<__nv_bfloat16>(__nv_bfloat16 x) { return __bfloat162float(x); }
+__device__ __forceinline__ float q8_ex2(float x) {  // relative error 2^-22, as the planes of the queries and weights
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
 template <typename T>
 __device__ __forceinline__ T from_float(float x);
 template <>

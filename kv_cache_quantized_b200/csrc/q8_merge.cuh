@@ -7,12 +7,6 @@ namespace axr {
 
 constexpr int kMergeWarps = 4;
 
-__device__ __forceinline__ float q8_ex2(float x) {  // relative error 2^-22, as the planes of the queries and weights
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
 // Merge of the n partials part(0) .. part(n - 1) of an output row by NW warps of a block: one, or all kMergeWarps, which
 // deal the partials among them and add their sums in warp order.  n = 0 gives zeros.
 template <typename T, int D, int NW, class Part>

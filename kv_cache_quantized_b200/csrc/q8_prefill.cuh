@@ -35,6 +35,7 @@
 
 #include "q8_attend.cuh"
 #include "tc.cuh"
+#include "warp_mma.cuh"
 
 namespace axr {
 
@@ -55,12 +56,6 @@ struct PrefillPlan {
   static constexpr int CH = D / 16;                        // 16-byte code chunks of a row
   static constexpr int NL = kPfKeys * CH / 128;            // chunks a converter thread holds of a tile
 };
-
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
 
 __device__ __forceinline__ float lg2(float x) {  // subnormal x included
   float y;
@@ -86,11 +81,6 @@ __device__ __forceinline__ bool elect_one() {
   uint32_t p;
   asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
   return p != 0;
-}
-
-__device__ __forceinline__ uint32_t pack_half2(float a, float b) {
-  const __half2 h = __floats2half2_rn(a, b);
-  return *reinterpret_cast<const uint32_t*>(&h);
 }
 
 // Shared-memory matrix descriptor with the 128-byte swizzle.
@@ -328,7 +318,7 @@ q8_prefill_kernel(const __grid_constant__ Q8Attend a, const Q8Tiles tl) {
         if (lane < 8) {
           scj[lane] = ks;
           scj[8 + lane] = off;
-          scj[16 + lane] = ex2(-off);
+          scj[16 + lane] = q8_ex2(-off);
         }
         if (lane == 0) scj[24] = lref;
       }
@@ -411,9 +401,9 @@ q8_prefill_kernel(const __grid_constant__ Q8Attend a, const Q8Tiles tl) {
       for (int e = 0; e < 16; e += 2) {
         const float2 y = fma2(make_float2(__uint_as_float(x[e]), __uint_as_float(x[e + 1])), make_float2(cc, cc),
                               make_float2(off, off));
-        const float2 p = make_float2(ex2(y.x), ex2(y.y));
+        const float2 p = make_float2(q8_ex2(y.x), q8_ex2(y.y));
         sum = add2(sum, p);
-        w[e >> 1] = pack_half2(p.x, p.y);
+        w[e >> 1] = pack_h2(p.x, p.y);
       }
       return sum.x + sum.y;
     };
@@ -461,11 +451,11 @@ q8_prefill_kernel(const __grid_constant__ Q8Attend a, const Q8Tiles tl) {
         }
         float alpha = 1.f;
         if (mx > m + static_cast<float>(kLazy)) {          // m = -inf: any finite maximum
-          alpha = m == -INFINITY ? 0.f : ex2(m - mx);
+          alpha = m == -INFINITY ? 0.f : q8_ex2(m - mx);
           m = mx;
         }
         l *= alpha;
-        alpha *= ex2(lref - top);
+        alpha *= q8_ex2(lref - top);
         lref = top;
         if (i > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
           if (!(ok = warp_wait(pv_done + 2 * q + ((i - 1) & 1), ((i - 1) >> 1) & 1))) break;
@@ -516,8 +506,8 @@ q8_prefill_kernel(const __grid_constant__ Q8Attend a, const Q8Tiles tl) {
     const bool live = threadIdx.x < nrow;
     const float nan = __uint_as_float(0x7fc00000u);
     // times 2^lref in two factors (one could leave fp32's normal range), times 2^-(15 - kLazy), over l; NaN stays
-    const float half = floorf(0.5f * lref), f2 = ex2(lref - half);
-    const float f1 = ex2(half - static_cast<float>(15 - kLazy)) / (a.splits == 1 && l != 0.f ? l : 1.f);
+    const float half = floorf(0.5f * lref), f2 = q8_ex2(lref - half);
+    const float f1 = q8_ex2(half - static_cast<float>(15 - kLazy)) / (a.splits == 1 && l != 0.f ? l : 1.f);
     const int64_t part = orow * a.splits + split;
 #pragma unroll 1
     for (int k = 0; k < D / 16; ++k) {
