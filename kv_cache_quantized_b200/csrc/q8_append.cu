@@ -66,7 +66,9 @@ __device__ __forceinline__ void q8_store(uint8_t* dst, const float (&x)[8], floa
       y[i] = z.x;
       y[i + 1] = z.y;
     }
-    if (finite) {
+    // below what magnitudes of 2^-100 need, an older scale may be too small for the new rows: x / s leaves the codes' reach,
+    // or 1 / s fp32's
+    if (finite && sc >= (I8 ? 6.3e-33f : 3.1e-33f)) {
       *reinterpret_cast<uint2*>(dst) = make_uint2(q8_pack4_finite<I8>(y), q8_pack4_finite<I8>(y + 4));
       return;
     }

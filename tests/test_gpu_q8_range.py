@@ -103,6 +103,30 @@ def test_attention_on_blocks_of_small_value_scale(dtype, counts):
     check(attend(bt_, pools), bt_, pools, "i8", 1 / math.sqrt(128), dtype, 4)
 
 
+# ---- appends onto tiny scales ----------------------------------------------------------------------------------------
+
+@pytest.mark.parametrize("kind", ["i8", "e4m3"])
+@pytest.mark.parametrize("old", [9.2e-41, 2.0 ** -130, 2.0 ** -120, 2.0 ** -108, 2.0 ** -107])
+@pytest.mark.parametrize("size", [0.0, 2.0 ** -125, 2.0 ** -101, 2.0 ** -99, 1.0])
+def test_appends_onto_older_tokens_under_a_tiny_scale(kind, old, size):
+    """A converted cache's older tokens under a scale below any that an append sets: the new codes are the formula's, bit
+    for bit, where 1 / s overflows (zeros stay zeros) and where x / s passes the largest code."""
+    d, Hkv, bt, n = 128, 2, 32, 3
+    rng = np.random.default_rng(21)
+    k, v = ((rng.uniform(0.5, 1, (n, Hkv, d)) * rng.choice([-1, 0, 1], (n, Hkv, d)) * size).astype(np.float32) for _ in "kv")
+    kc, vc = (rng.integers(0, 100, (2, Hkv, bt, d)).astype(np.uint8) for _ in "kv")
+    ks, vs = (np.full((2, Hkv, 2), old, np.float32) for _ in "kv")
+    dev = [cuda(a) for a in (kc, ks, vc, vs)]
+    table, lens = np.array([[1]], np.int32), [8 + n]
+    ops.q8_append_paged(cuda(k), cuda(v), *dev, cuda(table), cuda(np.array(lens, np.int32)), kind=kind,
+                        cu_new=cuda(np.array([0, n], np.int32)))
+    with np.errstate(over="ignore", invalid="ignore", under="ignore"):
+        q8.append([k], kc, ks, table, lens, [n], bt, kind)
+        q8.append([v], vc, vs, table, lens, [n], bt, kind)
+    for name, a, w in zip(("kcodes", "kscales", "vcodes", "vscales"), dev, (kc, ks, vc, vs)):
+        assert np.array_equal(a.cpu().numpy().view(np.uint8), w.view(np.uint8)), name
+
+
 # ---- queries ---------------------------------------------------------------------------------------------------------
 
 @pytest.mark.parametrize("dtype,counts", [f for f in FORMS if f[0] != "f16"])
