@@ -38,8 +38,9 @@ struct Q8Span {
   __device__ __forceinline__ int keys(int T) const { return min(pos0 + count, T); }
 };
 
-// From the entries cu[b], cu[b + 1] and the length.  Entries that make no sense, or a length out of range, set the status
-// word; a sequence of such entries counts as empty.
+// From the entries cu[b], cu[b + 1] and the length.  A sequence whose entries make no sense counts as empty; such entries,
+// or a length out of range, set the status word (FLAG).
+template <bool FLAG = true>
 __device__ __forceinline__ Q8Span q8_span_of(const Q8Attend& a, int64_t lo, int64_t hi, int len) {
   Q8Span s;
   bool bad = false;
@@ -50,13 +51,15 @@ __device__ __forceinline__ Q8Span q8_span_of(const Q8Attend& a, int64_t lo, int6
   s.first = lo;
   s.count = static_cast<int>(hi - lo);
   s.pos0 = max(len, 0) - s.count;
-  if (bad || (s.count > 0 && (len < 0 || len > a.T))) atomicOr(a.status, kStatusBadIndex);
+  if (FLAG && (bad || (s.count > 0 && (len < 0 || len > a.T)))) atomicOr(a.status, kStatusBadIndex);
   return s;
 }
 
+template <bool FLAG = true>
 __device__ __forceinline__ Q8Span q8_span(const Q8Attend& a, int b) {
   const int len = a.seq_lens ? a.seq_lens[b] : a.T;
-  return a.cu ? q8_span_of(a, a.cu[b], a.cu[b + 1], len) : q8_span_of(a, b, static_cast<int64_t>(b) + 1, len);
+  return a.cu ? q8_span_of<FLAG>(a, a.cu[b], a.cu[b + 1], len)
+              : q8_span_of<FLAG>(a, b, static_cast<int64_t>(b) + 1, len);
 }
 
 // How a kernel cuts the query tokens into row tiles of up to tpt tokens (times the heads of a group).

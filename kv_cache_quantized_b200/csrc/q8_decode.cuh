@@ -142,16 +142,16 @@ struct Q8Flat {
     r.ext.tiles = __shfl_sync(0xffffffffu, e.tiles, src);
   }
 
-  // The first sequence for which pick(b, tiles before, tiles of) holds; x < total and b < B always have one.
-  template <class Pick>
-  __device__ __forceinline__ Q8Place find(const Q8Attend& a, const Q8Tiles& tl, int lane, Pick pick) const {
+  // The sequence that holds flat tile x < total.
+  __device__ __forceinline__ Q8Place at_tile(const Q8Attend& a, const Q8Tiles& tl, int lane, int64_t x) const {
+    const auto pick = [=](int64_t ex_, int64_t n_) { return ex_ <= x && x < ex_ + n_; };
     Q8Place r;
-    unsigned who = __ballot_sync(0xffffffffu, pick(lane, ex[0], n[0]));
+    unsigned who = __ballot_sync(0xffffffffu, pick(ex[0], n[0]));
     if (who) {
       take(r, sp[0], ext[0], ex[0], 0, __ffs(who) - 1);
       return r;
     }
-    who = __ballot_sync(0xffffffffu, a.B > 32 && pick(32 + lane, ex[1], n[1]));
+    who = __ballot_sync(0xffffffffu, a.B > 32 && pick(ex[1], n[1]));
     if (who) {
       take(r, sp[1], ext[1], ex[1], 32, __ffs(who) - 1);
       return r;
@@ -160,11 +160,11 @@ struct Q8Flat {
     for (int b0 = 64; b0 < a.B; b0 += 32) {
       Q8Span s;
       Q8Extent e;
-      int64_t x, y;
-      scan(a, tl, lane, b0, sum, s, e, x, y);
-      who = __ballot_sync(0xffffffffu, pick(b0 + lane, x, y));
+      int64_t x0, y;
+      scan(a, tl, lane, b0, sum, s, e, x0, y);
+      who = __ballot_sync(0xffffffffu, pick(x0, y));
       if (who) {
-        take(r, s, e, x, b0, __ffs(who) - 1);
+        take(r, s, e, x0, b0, __ffs(who) - 1);
         return r;
       }
     }
@@ -174,13 +174,37 @@ struct Q8Flat {
     r.ext = {0, 1};
     return r;
   }
-  __device__ __forceinline__ Q8Place at_tile(const Q8Attend& a, const Q8Tiles& tl, int lane, int64_t x) const {
-    return find(a, tl, lane, [=](int, int64_t ex_, int64_t n_) { return ex_ <= x && x < ex_ + n_; });
-  }
-  __device__ __forceinline__ Q8Place of(const Q8Attend& a, const Q8Tiles& tl, int lane, int b) const {
-    return find(a, tl, lane, [=](int c, int64_t, int64_t) { return c == b; });
-  }
 };
+
+__device__ __forceinline__ int64_t q8_warp_sum(int64_t v) {
+#pragma unroll
+  for (int m = 16; m > 0; m >>= 1) v += __shfl_xor_sync(0xffffffffu, v, m);
+  return v;
+}
+
+// Sequence b in the flat tile sequence, and the tiles of all: sums instead of a search where b is known.
+__device__ __forceinline__ Q8Place q8_place(const Q8Attend& a, const Q8Tiles& tl, int lane, int b, int64_t& total) {
+  int64_t all = 0, before = 0;
+  Q8Span own{0, 0, 0};  // sequence b's, in lane b % 32
+#pragma unroll 2
+  for (int c = lane; c < a.B; c += 32) {
+    const Q8Span sp = q8_span<false>(a, c);
+    const Q8Extent e = q8_extent(a, tl, sp);
+    const int64_t n = static_cast<int64_t>(e.rts) * a.Hkv * e.tiles;
+    all += n;
+    before += c < b ? n : 0;
+    if (c == b) own = sp;
+  }
+  total = q8_warp_sum(all);
+  Q8Place r;
+  r.b = b;
+  r.begin = q8_warp_sum(before);
+  r.sp.first = __shfl_sync(0xffffffffu, own.first, b & 31);
+  r.sp.count = __shfl_sync(0xffffffffu, own.count, b & 31);
+  r.sp.pos0 = __shfl_sync(0xffffffffu, own.pos0, b & 31);
+  r.ext = q8_extent(a, tl, r.sp);
+  return r;
+}
 
 __device__ __forceinline__ int64_t q8_share(int64_t total, int workers) {
   const int64_t s = q8_div(total + workers - 1, workers);
@@ -569,15 +593,14 @@ q8_decode_merge_kernel(const __grid_constant__ Q8Attend a, const __grid_constant
   int b;
   int64_t i0;
   q8_tile(a, tl, unit / a.Hkv, lane, b, i0);
-  Q8Flat flat;
-  flat.load(a, tl, lane);
-  const Q8Place at = flat.of(a, tl, lane, b);
+  int64_t total;
+  const Q8Place at = q8_place(a, tl, lane, b, total);
   const Q8Span sp = at.sp;
   // every block waits, those without a row too: this grid's end stands for the attention kernel's
   const auto wait = [] { asm volatile("griddepcontrol.wait;\n" ::: "memory"); };
   if (!q8_tile_live(a, tl, sp, i0, threadIdx.x)) return wait();
   if (r >= min(tl.tpt, sp.count - static_cast<int>(i0)) * a.G) return wait();
-  const int64_t S = q8_share(flat.total, workers);
+  const int64_t S = q8_share(total, workers);
   const Q8Extent ext = at.ext;
   const int64_t p0 = at.begin + (q8_div(i0, tl.tpt) * a.Hkv + hk) * ext.tiles, p1 = p0 + ext.tiles;  // the unit's flat tiles
   const int w0 = static_cast<int>(q8_div(p0, S)), n = p1 > p0 ? static_cast<int>(q8_div(p1 - 1, S)) - w0 + 1 : 0;
