@@ -76,6 +76,7 @@ append_kernel(const __grid_constant__ PagedNew p, const __grid_constant__ Append
               int q_parts) {
   constexpr int VPL = D / 32, R = D * BITS / 8;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  if (check_offsets(p)) return;
   const int64_t unit = static_cast<int64_t>(blockIdx.x) * kWarps + warp;
   if (unit >= kv_units) {
     const int64_t u = unit - kv_units;
@@ -135,7 +136,7 @@ template <typename T, int D, int BITS, bool VQ, int KH>
 axr_status launch_kh(const PagedNew& p, const AppendArgs& a, cudaStream_t st, const char* w) {
   const int kv_parts = (a.Hkv + KH - 1) / KH, q_parts = a.q ? (a.Hq + query_slice(D) - 1) / query_slice(D) : 0;
   const int64_t kv_units = p.n_tok * kv_parts, units = kv_units + p.n_tok * q_parts;
-  const int64_t grid = (units + kWarps - 1) / kWarps;
+  const int64_t grid = (units + kWarps - 1) / kWarps + (p.cu ? 1 : 0);  // check_offsets
   if (grid > 0x7fffffff) return set_error(AXR_EUNSUPPORTED, "%s: too many tokens and heads for one call", w);
   append_kernel<T, D, BITS, VQ, KH>
       <<<static_cast<unsigned>(grid), kThreads, 0, st>>>(p, a, kv_units, kv_parts, q_parts);

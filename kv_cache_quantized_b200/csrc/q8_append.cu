@@ -95,6 +95,7 @@ q8_append_kernel(const __grid_constant__ PagedNew p, const __grid_constant__ Q8A
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int sub = lane / P::LPR, e0 = 8 * (lane % P::LPR);
 
+  if (check_offsets(p)) return;
   if (blockIdx.x >= kv_blocks) {
     const int64_t u = (blockIdx.x - kv_blocks) * (kAppendThreads / 32) + warp;
     if (q_parts == 0 || u >= p.n_tok * q_parts) return;
@@ -226,7 +227,8 @@ axr_status launch(bool i8, const PagedNew& p, const Q8AppendArgs& a, cudaStream_
   constexpr int warps = kAppendThreads / 32;
   const int kv_parts = (a.Hkv + Q8AppendPlan<D>::HPC - 1) / Q8AppendPlan<D>::HPC;
   const int q_parts = a.q ? (a.Hq + query_slice(D) - 1) / query_slice(D) : 0;
-  const int64_t kv_blocks = items * kv_parts, grid = kv_blocks + (p.n_tok * q_parts + warps - 1) / warps;
+  const int64_t kv_blocks = items * kv_parts;
+  const int64_t grid = kv_blocks + (p.n_tok * q_parts + warps - 1) / warps + (p.cu ? 1 : 0);  // check_offsets
   if (grid > 0x7fffffff) return set_error(AXR_EUNSUPPORTED, "%s: too many tokens and heads for one call", w);
   const unsigned g = static_cast<unsigned>(grid);
   if (i8) q8_append_kernel<T, D, true><<<g, kAppendThreads, 0, st>>>(p, a, kv_blocks, kv_parts, q_parts);
