@@ -48,17 +48,20 @@ Q8Plan plan_decode(int64_t n_tok, int B, int G, int Hkv, int T, bool one, int ma
 
 constexpr int64_t kMaxPartials = 16 * kSmCount * kQ8PrefillRows;  // 315 MB of workspace at d = 128
 
-// The tcgen05 kernel: tiles of 256 rows, one thread block per SM, a tile a sequence where max_q allows it.  In units of
-// one key tile (128 tokens), a block's set-up (query operand, first code tiles) costs about 2, and writing and merging
-// the partials of a split axis up to 3 more: a full tile's 256 x d fp32 rows cross HBM twice.  The host knows no
-// lengths: how many tiles have work is estimated, with every sequence, or, beside a launch for those of up to `few`
-// tokens, as many longer ones as there must be.  (A count of the numbered tiles instead of those with work split 148
-// units of 64 key tiles in four: 173 against 117 us.)  The workspace holds a partial for each query row and split, and a
-// split stops at kMaxPartials of them.  (A bound on the numbered tiles, with work or without, left a chunk of 64 tokens
-// on 32768 keys beside 199 single tokens in one piece: 751 against 450 us.)
-// Beside short sequences most blocks have no work: they cost about one unit a wave of SMs and split, and from 9 splits on,
-// where the merge takes a block a row, 0.65 for 16 such blocks an SM (59 single tokens and the chunk: 8 splits 184 us, 10
-// splits 251 us; 15 single tokens: 16 splits 112 us, 8 splits 120 us).
+// The tcgen05 kernel: tiles of 256 rows, one thread block per SM, a tile a sequence where max_q allows it.  The split of
+// the token axis minimises an estimate in units of one key tile (128 tokens, about 2 us of a full row tile):
+//   waves (keys / splits + 5.5 + 5.4 fill) + 2.1   with fill the rows in use of a tile, the last two terms if split,
+// fitted to 66 calls of 1 to 16 sequences and 16 to 4096 tokens each on 2048 to 32768 keys, timed at up to nine splits
+// (7 % rms; the choice is 0.5 % above the best split on average, 9 % at most.  An estimate with 2 and 3 fill in their
+// places split two chunks of 2048 on 8192 keys, 459 us, in two, 583 us).  The host knows no lengths: sequences are taken
+// to be T long, and how many tiles have work is estimated, with every sequence, or, beside a launch for those of up to
+// `few` tokens, as many longer ones as there must be.  (A count of the numbered tiles instead of those with work split 148
+// units of 64 key tiles in four: 173 against 117 us.)
+// Blocks without work cost about one unit a wave of SMs and split, and from 9 splits on, where the merge takes a block a
+// row, a row costs 53 / 10^5, one without work half of it (59 single tokens and a chunk of 64 on 32768 keys: 8 splits
+// 184 us, 10 splits 251 us; 15 single tokens: 16 splits 112 us, 8 splits 120 us).
+// The workspace holds a partial for each query row and split, and a split stops at kMaxPartials of them.  (A bound on the
+// numbered tiles, with work or without, left the chunk beside 199 single tokens in one piece: 751 against 415 us.)
 Q8Plan plan_prefill(int64_t n_tok, int B, int G, int Hkv, int T, int max_q, int few) {
   Q8Plan pl;
   pl.nrg = kQ8PrefillRows / 8;
@@ -70,20 +73,20 @@ Q8Plan plan_prefill(int64_t n_tok, int B, int G, int Hkv, int T, int max_q, int 
   const int64_t least = std::max<int64_t>(1, (n_tok - static_cast<int64_t>(few) * B + max_q - 1) / max_q);
   const int64_t seqs = few ? least : B;
   const int64_t live =
-      pl.tl.one ? seqs : std::min(n_tok / pl.tl.tpt + seqs, static_cast<int64_t>(B) * ((max_q - 1) / pl.tl.tpt + 1));
-  const int64_t units = live * Hkv, total = (static_cast<int64_t>(T) + 127) / 128;
+      pl.tl.one ? seqs : std::min(n_tok / pl.tl.tpt + seqs, seqs * ((max_q - 1) / pl.tl.tpt + 1));
+  const int64_t units = live * Hkv, total = (static_cast<int64_t>(T) + 127) / 128, rows = n_tok * G * Hkv;
   const double fill = std::min(1.0, static_cast<double>(n_tok) * G / (static_cast<double>(live) * kQ8PrefillRows));
-  const auto waves = [&](int64_t s) { return static_cast<double>((units * s + kSmCount - 1) / kSmCount); };
+  const double keys = std::max(0.0, T - 0.5 * static_cast<double>(n_tok) / B) / 128;  // causal rows: half of the new ones
   const double idle = static_cast<double>(pl.tl.tiles * Hkv - units) / kSmCount;
-  const double idle_rows = 0.65 / 16 * idle * std::min(max_q, pl.tl.tpt) * G;
-  pl.sp.splits = 1;
-  pl.sp.chunk = static_cast<int>(total * 128);
-  double best = waves(1) * (total + 2) + idle;
-  const int64_t rows = n_tok * G * Hkv;
-  for (int64_t s = 2; s <= total / 2 && s <= 256 && rows * s <= kMaxPartials; ++s) {
+  const double idle_rows = idle * kSmCount * std::min(max_q, pl.tl.tpt) * G;
+  double best = 0;
+  for (int64_t s = 1; s == 1 || (s <= total / 2 && s <= 256 && rows * s <= kMaxPartials); ++s) {
     const int64_t per = (total + s - 1) / s, splits = (total + per - 1) / per;
-    const double cost = waves(splits) * (per + 2 + 3 * fill) + idle * splits + (splits > 8 ? idle_rows : 0.0);
-    if (cost < best) {
+    const double waves = static_cast<double>((units * splits + kSmCount - 1) / kSmCount);
+    double cost = waves * (std::min(static_cast<double>(per), keys / splits) + 5.5) + idle * splits;
+    if (splits > 1) cost += waves * 5.4 * fill + 2.1;
+    if (splits > 8) cost += 53e-5 * (rows + 0.5 * idle_rows);
+    if (s == 1 || cost < best) {
       best = cost;
       pl.sp.splits = static_cast<int>(splits);
       pl.sp.chunk = static_cast<int>(per * 128);
