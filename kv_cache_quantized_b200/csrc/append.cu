@@ -7,7 +7,7 @@
 // its token's place in the cache is known.  The codes equal axr_write_keys' for the rotated key, bit for bit: the same
 // quantize_lane on the same fp32 values.  KH = 4 keeps 2 KB a warp in flight on long calls; short calls take KH = 1, a
 // head a warp (chunks of 8192 fp16 tokens into 32 / 8 heads of d = 128, b = 4, fp16 values: 56 us against 76 us with
-// KH = 1; a step of 8 tokens 3.5 us).  Issue slots bound the quantized heads (about 250 instructions a vector, 64 % of
+// KH = 1; a step of 8 tokens 3.8 us).  Issue slots bound the quantized heads (about 250 instructions a vector, 64 % of
 // the slots busy), HBM traffic the query and fp16 value rows (243 MB: 4.3 TB/s, 0.66 of the copy rate), launch latency
 // single tokens.
 #include "axr_host.h"

@@ -6,8 +6,8 @@
 // block's largest magnitude goes through one redux per warp and head and a shared-memory maximum; then
 //   s = max(s_old, need(amax)),  code = rne(x * (1 / s)),  and, where s grew, older codes = rne(code * (s_old * (1 / s)))
 // so a scale block is one work item, whatever mix of older and new tokens it holds, and no atomics on global memory
-// are needed.  Issue slots (67 %) and HBM traffic together bound long calls: q, k and v are read once and q, codes and
-// scales written once, 8 x 2048 fp16 tokens of 32 / 8 heads (349 MB) in 67 us, 5.2 TB/s or 0.79 of the copy rate (two
+// are needed.  Issue slots (72 %) and HBM traffic together bound long calls: q, k and v are read once and q, codes and
+// scales written once, 8 x 2048 fp16 tokens of 32 / 8 heads (349 MB) in 68 us, 5.1 TB/s or 0.78 of the copy rate (two
 // heads a warp and four blocks an SM; four heads and two blocks: 78 us).  A step of single tokens is three round trips to
 // memory (the sequence's entries; its table entry, rows and rotation; the scales): 6 us for 64 sequences.
 #include "axr_host.h"

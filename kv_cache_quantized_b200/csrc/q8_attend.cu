@@ -21,9 +21,9 @@ struct Q8Plan {
 // Sequences of few query rows among longer ones (decoding sequences in a batch of prompt chunks): the warp-MMA kernel
 // takes those of up to 8 rows (one token from 8 heads of a group on) and the tcgen05 kernel, which would run a 256-row
 // tile for each, the others.  The host knows no lengths, so the second launch is made where the mean length is below
-// half of the longest (32 / 8 heads, d = 128, bf16: 63 single tokens and a chunk of 512 on up to 4096 keys 199 -> 151 us,
-// 31 and a chunk of 2048 186 -> 165 us, 32 single tokens without a bound on max_q 96 -> 51 us; four ragged chunks, none
-// of them short, 3 us more).
+// half of the longest (32 / 8 heads, d = 128, bf16: 63 single tokens and a chunk of 512 on up to 4096 keys 192 -> 149 us,
+// 31 and a chunk of 2048 180 -> 162 us, 32 single tokens without a bound on max_q 94 -> 52 us; four ragged chunks, none
+// of them short, 168 -> 171 us).
 int short_tokens(int64_t n_tok, int B, int max_q, int G) {
   if (2 * n_tok >= static_cast<int64_t>(B) * max_q) return 0;
   return G <= 8 ? 8 / G : 1;

@@ -17,15 +17,15 @@
 //   O^T += V^T P^T A = 16 coordinates x 16 tokens of codes, B = the weights, transposed in registers (movmatrix).
 // The codes enter exactly; queries as PQ fp16 planes, hi and lo (about 22 bits) for fp32, one for 16-bit types, which a
 // power of two makes exact; softmax weights as PP planes, one for bf16 (a rounding to 2^-11, where the output's is 2^-9),
-// hi and lo for fp16 and fp32.  Coordinates and tokens may
-// be summed in any order, so each lane reads 16-byte runs of a code row: of the key rows 8 n + g the bytes
-// [D/4 t, D/4 t + D/4), whose word s feeds k-step s; of the value rows 2 t, 2 t + 1, 2 t + 8, 2 t + 9 (+ 16) the bytes
-// [D/8 g, D/8 g + D/8), bytes 2 j and 2 j + 1 going to rows g and g + 8 of coordinate tile j.  Every code is read from
-// shared memory once, by 128-bit loads that the swizzle keeps free of bank conflicts.
+// hi and lo for fp16 and fp32; no plane holds less than 2^-24, so a token's value is within 2^-38 of the largest scale.
+// Coordinates and tokens may be summed in any order, so each lane reads 16-byte runs of a code row: of the key rows
+// 8 n + g the bytes [D/4 t, D/4 t + D/4), whose word s feeds k-step s; of the value rows 2 t, 2 t + 1, 2 t + 8, 2 t + 9
+// (+ 16) the bytes [D/8 g, D/8 g + D/8), bytes 2 j and 2 j + 1 going to rows g and g + 8 of coordinate tile j.  Every
+// code is read from shared memory once, by 128-bit loads that the swizzle keeps free of bank conflicts.
 // (tcgen05 would need the codes as fp16 in shared memory, four times this traffic, for 4 to 16 query rows of 128.)
 //
-// HBM bounds long calls: 8 sequences x 32768 tokens, 32 / 8 heads, d = 128 take 96-100 us with the merge, 5.4-5.6 TB/s
-// or 0.82-0.86 of the copy rate (94 us without the merge); the same batch with 16 query heads per KV head (two row
+// HBM bounds long calls: 8 sequences x 32768 tokens, 32 / 8 heads, d = 128 take 96-103 us with the merge, 5.2-5.6 TB/s
+// or 0.80-0.85 of the copy rate; the same batch with 16 query heads per KV head (two row
 // groups) is bound by issue slots.  Small calls are a chain of round trips: lengths, block table, tiles, partials (one
 // sequence of 4096 tokens: 12 us, 8 without the merge).  With the query rows as the M side, hi and lo planes stacked in
 // one tile, the long call took 121 us: twice the MMAs and accumulators, eight warps instead of twelve.

@@ -25,9 +25,9 @@
 // scaled by), so the output is seldom rescaled, and a tile takes one pass over S: the weights are formed with the
 // present maximum and kept in registers until the tile's own maximum is known.
 //
-// Measured, 4 sequences x 2048 query tokens over up to 8192 keys, 32 / 8 heads, d = 128 (0.96 Tflop): 930-980 us, about
-// 1.0 PFLOP/s, 0.61-0.64 of the bf16 GEMM rate.  Nothing is saturated: tensor pipe 52 %, exponentials 53 %, issue slots
-// 56 % of the active cycles; without its MMAs, its exponentials or its conversions the kernel is 6-9 % faster each, so
+// Measured, 4 sequences x 2048 query tokens over up to 8192 keys, 32 / 8 heads, d = 128 (0.96 Tflop): 920-990 us, about
+// 1.0 PFLOP/s, 0.60-0.65 of the bf16 GEMM rate.  Nothing is saturated: tensor pipe 55 %, exponentials 55 %, issue slots
+// 59 % of the active cycles; without its MMAs, its exponentials or its conversions the kernel is 6-9 % faster each, so
 // the chain of hand-overs (a satisfied mbarrier wait costs a warp about 170 clocks) bounds it.  Slower forms: one S of 128
 // keys a row tile (1093 us), one issuing warp for all products (1366 us), one a row tile (1024 us), all 64 columns of a
 // step loaded at once (1044 us), two threads a row (1124 us).
