@@ -24,8 +24,8 @@
 // code is read from shared memory once, by 128-bit loads that the swizzle keeps free of bank conflicts.
 // (tcgen05 would need the codes as fp16 in shared memory, four times this traffic, for 4 to 16 query rows of 128.)
 //
-// HBM bounds long calls: 8 sequences x 32768 tokens, 32 / 8 heads, d = 128 take 96-103 us with the merge, 5.2-5.6 TB/s
-// or 0.80-0.85 of the copy rate; the same batch with 16 query heads per KV head (two row
+// HBM bounds long calls: 8 sequences x 32768 tokens, 32 / 8 heads, d = 128 take 94-103 us with the merge, 5.2-5.7 TB/s
+// or 0.80-0.87 of the copy rate; the same batch with 16 query heads per KV head (two row
 // groups) is bound by issue slots.  Small calls are a chain of round trips: lengths, block table, tiles, partials (one
 // sequence of 4096 tokens: 12 us, 8 without the merge).  With the query rows as the M side, hi and lo planes stacked in
 // one tile, the long call took 121 us: twice the MMAs and accumulators, eight warps instead of twelve.
