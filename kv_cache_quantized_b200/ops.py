@@ -517,7 +517,8 @@ def q8_attend_paged(q, kcodes, kscales, vcodes, vscales, block_table, seq_lens=N
     q [n_tok, Hq, d] (float16, bfloat16 or float32; token rows may be strided): sequence b's query tokens are
     cu_q[b] .. cu_q[b+1] - 1 (int32 [B+1]; None: one per sequence, a decode step), the last positions of its seq_lens[b];
     each sees the cache up to its own position.  max_q (optional) bounds a sequence's query tokens, T (default
-    max_blocks * bt) its length.  Returns out [n_tok, Hq, d] in q's dtype."""
+    max_blocks * bt) its length: tight ones pick the better kernel and split.  A longer sequence's tokens see no key at or
+    past T, which device_status() shows.  Returns out [n_tok, Hq, d] in q's dtype."""
     return (_ext or _paged()).q8_attend_paged(q, kcodes, kscales, vcodes, vscales, block_table, seq_lens,
                                               _q8_kind(kind), cu_q, max_q, T, scale, out, workspace)
 
