@@ -431,8 +431,8 @@ AXR_API axr_status axr_pot_attend_decode(const float* q, const uint8_t* codes, c
  *   gets 0.
  *   max_q an upper bound of a sequence's query tokens, or 0 if unknown (a tight one picks the better kernel); rows of a
  *   sequence with more may stay unwritten, which sets AXR_STATUS_BAD_INDEX.  T an upper bound of the lengths (a tight
- *   one picks the better split); seq_lens NULL: all T.  A longer sequence's tokens keep their positions, but see no key at or past T, which sets
- *   AXR_STATUS_BAD_INDEX.
+ *   one picks the better split); seq_lens NULL: all T.  A longer sequence's tokens keep their positions, but see no key
+ *   at or past T, which sets AXR_STATUS_BAD_INDEX.
  *   A table entry outside [0, num_blocks) reads block 0 and sets AXR_STATUS_BAD_INDEX.  Cache rows at or past a
  *   sequence's length may hold anything.  G = Hq / Hkv in 1 .. 16.
  *   workspace [dev] >= axr_q8_attend_workspace_bytes(n_tok, max_q, B, Hq, Hkv, T, d) bytes (max_q = 1 without cu_q),
